@@ -252,9 +252,12 @@ FB_API fb_status fb_gemv_group_scales(const fb_weights *W, int G, const void *x,
 FB_API fb_status fb_gemv_launch_plan(const fb_weights *W, int batch, unsigned flags, int sms, int *out);
 
 /* fb_device_errors: synchronises the current device, then stores in *flags
- * the error bits GEMV kernels have raised since the last clear (bit 0: a CTA
- * gave up its bounded wait for the row partials of its cluster; the rows it
- * owns were written as NaN), and clears them when clear != 0.  Returns
+ * the error bits kernels have raised since the last clear (bit 0: a CTA of a
+ * GEMV gave up its bounded wait for the row partials of its cluster; the rows
+ * it owns were written as NaN; bit 1: fb_attn_tree met a page outside the
+ * cache or a sequence of too many drafted tokens; bit 2: a CTA of an attention
+ * call gave up a bounded wait, its rows were not written), and clears them
+ * when clear != 0.  Returns
  * FB_ERR_INVALID_VALUE for a null flags, FB_ERR_CUDA if the device reports an
  * error, else FB_OK. */
 FB_API fb_status fb_device_errors(unsigned int *flags, int clear);
@@ -297,6 +300,106 @@ FB_API fb_status fb_fit_saliency(const float *W, int M, int N, int ldw, const fl
  * M <= 2^24, N <= 2^20.  Errors as fb_fit_saliency. */
 FB_API fb_status fb_fit_base(float *R, int M, int N, int ldr, int sweeps, int8_t *signs, int lds, float *alpha_r,
                              float *alpha_c, void *stream);
+
+/* ---- A decoder layer's attention, between the q/k/v and the o GEMV --------
+ * Three calls: fb_qk_norm_rope takes the projected heads to their positions
+ * and puts keys and values into a paged cache; fb_attn_prompt is the causal
+ * attention of whole prompts; fb_attn_tree is the attention of single tokens
+ * and of trees of drafted tokens over the cache.  All are asynchronous on
+ * `stream`, deterministic, and keep every norm, score, softmax sum and
+ * accumulated output in fp32.  flags: 0 or FB_GEMV_PDL (the kernel may be
+ * launched before the previous one ends; it reads and writes nothing before
+ * that one has completed).  Pointers are 16-byte aligned unless stated
+ * otherwise, row pitches (ld*, in elements) multiples of 16 bytes.
+ * Limits: 1 <= T <= 2^24, 1 <= Hq <= 1024, Hkv divides Hq. */
+
+/* The heads of T tokens: head h of token i is the D consecutive elements at
+ * q + i*ldq + h*D (Hq heads), k + i*ldk + h*D and v + i*ldv + h*D (Hkv
+ * heads); query head h reads key head h / (Hq / Hkv).  Slices of one fused
+ * projection are described by their pitch.  Host struct, device pointers. */
+typedef struct fb_heads {
+    void *q, *k, *v;
+    fb_dtype t;
+    int T, Hq, Hkv, D;
+    int ldq, ldk, ldv;
+} fb_heads;
+
+/* A layer's paged cache: k and v are [pages][Hkv][page_size][D] of type t
+ * (FB_F16 or FB_BF16), page_size a power of two <= 1024, pages * page_size <
+ * 2^31.  Slot s is row s % page_size of page s / page_size. */
+typedef struct fb_kv_cache {
+    void *k, *v;
+    fb_dtype t;
+    int pages, page_size, Hkv, D;
+} fb_kv_cache;
+
+/* fb_qk_norm_rope: for every token i and head h,
+ *   x' = x * w / sqrt(mean_d(x_d^2) + eps)     (w = q_weight for queries,
+ *        k_weight for keys: D floats; NULL leaves those heads unnormed)
+ *   rotation of the first rot elements of x' by angle_p = pos[i]*inv_freq[p]
+ *   for pair p < rot/2, (a, b) -> (a cos - b sin, b cos + a sin), the pair
+ *   being elements (p, p + rot/2), or with FB_ROPE_NEIGHBOURS (2p, 2p + 1);
+ *   values are only converted.
+ * in->t: any type; out->t: FB_F16 or FB_BF16, the same T, Hq, Hkv, D.  Each of
+ * out->q, out->k, out->v may be NULL (not written) or the input itself when
+ * type and pitch agree (in place); otherwise they must not overlap the
+ * inputs.  cache (may be NULL; type out->t) takes token i's keys and values
+ * at slot slots[i]; a slot outside [0, pages*page_size) is skipped, and the
+ * same slot twice leaves either token's elements.  pos: T int32, any sign;
+ * inv_freq: rot/2 doubles (8-byte aligned); angles are reduced in fp64, so a
+ * far position is as exact as a near one.  D a multiple of 16, <= 256; rot a
+ * multiple of 16, 0 <= rot <= D (inv_freq, pos may be NULL when 0).  eps >= 0.
+ * Each output is rounded once from fp32. */
+#define FB_ROPE_NEIGHBOURS 0x10u
+FB_API fb_status fb_qk_norm_rope(const fb_heads *in, const fb_heads *out, const int32_t *pos, const double *inv_freq,
+                                 int rot, const float *q_weight, const float *k_weight, float eps,
+                                 const fb_kv_cache *cache, const int32_t *slots, unsigned flags, void *stream);
+
+/* fb_attn_prompt: causal attention of n packed sequences.  Sequence s is the
+ * tokens cu_seqlens[s] .. cu_seqlens[s+1]-1 (n + 1 int32 on the device, not
+ * descending, first >= 0, last <= T; values outside are clamped); token i of it
+ *   out_i = sum_{j <= i} p_ij v_j,   p_ij = softmax_j(scale * q_i . k_j).
+ * in->t: FB_F16 or FB_BF16; D = 64 or 128; scale > 0.  out: T rows of Hq*D
+ * elements of type in->t with pitch ldo, not overlapping the inputs; lse (may
+ * be NULL, 4-byte aligned): [T][Hq] fp32, log sum_j exp(scale * q_i . k_j).
+ * Rows of no sequence keep their contents.  What lies outside a sequence, and
+ * later tokens within it, never reaches a row, whatever the values (NaN and
+ * infinity included).  The weights p are rounded to in->t before they meet v
+ * (the tensor cores take operands of one type), their sum is of fp32 values. */
+FB_API fb_status fb_attn_prompt(const fb_heads *in, const int32_t *cu_seqlens, int n, float scale, void *out, int ldo,
+                                float *lse, unsigned flags, void *stream);
+
+/* fb_attn_tree: attention of each sequence's newest tokens over the cache.
+ * Sequence s (s < n) has lens[s] >= 0 committed keys and the drafted tokens
+ * cu_draft[s] .. cu_draft[s+1]-1 of q (n + 1 int32; NULL: one token each,
+ * T = n), m_s <= max_draft <= 64 of them.  Key position p of the sequence,
+ * p < lens[s] + m_s, is in the cache at row p % page_size of page
+ * page_table[s*ld_table + p / page_size]; positions lens[s] + j hold the
+ * drafted tokens' own keys (put there by fb_qk_norm_rope).  Drafted token i
+ * sees every committed key, and drafted token j where bit j of
+ * mask[cu_draft[s] + i] is set (bits >= m_s are ignored); mask NULL: j <= i,
+ * a chain.  A row that sees nothing gives zeros and lse = -infinity.
+ * page_table: n rows of table_width pages, pitch ld_table >= table_width.
+ * q: T rows of Hq*D elements of the cache's type, pitch ldq; out likewise with
+ * pitch ldo, not overlapping q; lse [T][Hq] fp32 or NULL; mask 8-byte, other
+ * integers 4-byte aligned.  D = 64 or 128; scale > 0; n <= 65536.
+ * Positions that a row does not see never reach it, whatever the cache holds
+ * there.  A page outside [0, pages), or a position beyond table_width pages,
+ * among the keys that a row sees gives NaN in that row, and a sequence of
+ * more than max_draft tokens leaves those behind them unwritten; both raise
+ * bit 1 of fb_device_errors, and no memory outside the cache is read.  Tokens
+ * of no sequence keep their contents.  The weights are rounded as in
+ * fb_attn_prompt.
+ * ws: fb_attn_tree_workspace_bytes bytes, 16-byte aligned, for the partial
+ * results of sequences split over several CTAs; its contents need not be
+ * set up and mean nothing afterwards, but calls that may run at the same
+ * time (on several streams, in several captured graphs) need one each.
+ * fb_attn_tree_workspace_bytes is host only; 0 for invalid sizes. */
+FB_API size_t fb_attn_tree_workspace_bytes(int Hq, int Hkv, int D, int max_draft);
+FB_API fb_status fb_attn_tree(const void *q, int ldq, int T, int Hq, const fb_kv_cache *cache,
+                              const int32_t *page_table, int table_width, int ld_table, const int32_t *lens,
+                              const int32_t *cu_draft, int n, int max_draft, const uint64_t *mask, float scale, void *out, int ldo, float *lse,
+                              void *ws, size_t ws_bytes, unsigned flags, void *stream);
 
 /* Human-readable name of a status code (static string). */
 FB_API const char *fb_status_string(fb_status s);

@@ -8,8 +8,8 @@ functions raises; there is no CPU fallback.
 
 Names follow the C ABI: fb_pack, fb_pack_bits, fb_unpack, fb_vcm_gather,
 fb_lut_build, fb_validate_weights, fb_gemv_workspace_bytes, fb_gemv,
-fb_gemv_batched; ``Weights`` wraps one fb_weights struct and the tensors it
-points to.
+fb_gemv_batched, fb_qk_norm_rope, fb_attn_prompt, fb_attn_tree; ``Weights``
+wraps one fb_weights struct and the tensors it points to.
 """
 
 from __future__ import annotations
@@ -26,6 +26,8 @@ __all__ = [
     "fb_lut_build", "fb_validate_weights", "fb_gemv_workspace_bytes", "fb_gemv",
     "fb_gemv_batched", "fb_status_string", "fb_gemv_launch_plan", "fb_gemv_grouped", "fb_device_errors",
     "fb_fit_saliency", "fb_fit_base", "fit", "fb_gemv_group_scales",
+    "FB_ROPE_NEIGHBOURS", "rope_frequencies", "fb_qk_norm_rope", "fb_attn_prompt", "fb_attn_tree",
+    "fb_attn_tree_workspace_bytes",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -35,6 +37,7 @@ FB_OK = 0
 FB_GEMV_PDL = 1
 FB_GEMV_INDEPENDENT = 2
 FB_GEMV_TEST_WAIT_TIMEOUT = 0x80000000
+FB_ROPE_NEIGHBOURS = 0x10
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _STATUS = {0: "FB_OK", 1: "FB_ERR_INVALID_VALUE", 2: "FB_ERR_UNSUPPORTED", 3: "FB_ERR_MISALIGNED",
            4: "FB_ERR_WORKSPACE", 5: "FB_ERR_CUDA"}
@@ -56,6 +59,21 @@ class FbWeightsStruct(C.Structure):
     ]
 
 
+class FbHeadsStruct(C.Structure):
+    _fields_ = [
+        ("q", C.c_void_p), ("k", C.c_void_p), ("v", C.c_void_p), ("t", C.c_int),
+        ("T", C.c_int), ("Hq", C.c_int), ("Hkv", C.c_int), ("D", C.c_int),
+        ("ldq", C.c_int), ("ldk", C.c_int), ("ldv", C.c_int),
+    ]
+
+
+class FbKvCacheStruct(C.Structure):
+    _fields_ = [
+        ("k", C.c_void_p), ("v", C.c_void_p), ("t", C.c_int),
+        ("pages", C.c_int), ("page_size", C.c_int), ("Hkv", C.c_int), ("D", C.c_int),
+    ]
+
+
 _lib = None
 
 
@@ -70,6 +88,7 @@ def lib() -> C.CDLL:
         L = C.CDLL(library_path)
         P, I, S = C.c_void_p, C.c_int, C.c_size_t
         W = C.POINTER(FbWeightsStruct)
+        H, KV, F, U = C.POINTER(FbHeadsStruct), C.POINTER(FbKvCacheStruct), C.c_float, C.c_uint
         sig = {
             "fb_packed_words": (S, [I, I, I]),
             "fb_pack": (I, [P, I, I, I, P, P]),
@@ -87,6 +106,10 @@ def lib() -> C.CDLL:
             "fb_device_errors": (I, [P, I]),
             "fb_fit_saliency": (I, [P, I, I, I, P, I, I, I, P, P, P]),
             "fb_fit_base": (I, [P, I, I, I, I, P, I, P, P, P]),
+            "fb_qk_norm_rope": (I, [H, H, P, P, I, P, P, F, KV, P, U, P]),
+            "fb_attn_prompt": (I, [H, P, I, F, P, I, P, U, P]),
+            "fb_attn_tree_workspace_bytes": (S, [I, I, I, I]),
+            "fb_attn_tree": (I, [P, I, I, I, KV, P, I, I, P, P, I, I, P, F, P, I, P, P, S, U, P]),
             "fb_status_string": (C.c_char_p, [I]),
             "fb_abi_version": (I, []),
         }
@@ -404,3 +427,163 @@ def fit(W: torch.Tensor, X: torch.Tensor, K: int, Ks: int, nS: int, sweeps: int)
     return {"signs": signs, "alpha_r": ar, "alpha_c": ac, "score": score, "s_idx": s_idx,
             "s_signs": s_signs[:, :, :nS], "s_alpha_r": s_ar, "s_alpha_c": s_ac[:, :nS], "residual": R,
             "s_residual": None if RS is None else RS[:, :nS]}
+
+
+# ---- attention ---------------------------------------------------------------
+
+
+def _on(device: torch.device, f, *args) -> int:
+    """f(*args, stream) on the device the tensors live on, whichever is current."""
+    if device.index is not None and device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return f(*args, _stream(device))
+    return f(*args, _stream(device))
+
+
+def _head_rows(t: torch.Tensor, what: str, device=None, shape=None, dtype=None) -> int:
+    """The row pitch of [T, H, D] heads whose heads are contiguous within a row."""
+    if t.dim() != 3 or t.dtype not in _DTYPES or t.device.type != "cuda":
+        raise ValueError(f"{what}: a [T, heads, D] tensor (f32/f16/bf16) on the GPU")
+    T, H, D = t.shape
+    if shape is not None and (T, H, D) != shape:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {shape}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{what}: {t.dtype}, expected {dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{what}: on {t.device}, expected {device}")
+    if (t.stride(2) != 1 and D > 1) or (t.stride(1) != D and H > 1):
+        raise ValueError(f"{what}: the heads of a row must be contiguous (only rows may be strided)")
+    return t.stride(0) if T > 1 else H * D
+
+
+def _flat(t: Optional[torch.Tensor], what: str, dtype, shape, device) -> Optional[int]:
+    """The address of a contiguous tensor of the given type and shape (None passes)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{what}: a contiguous {dtype} tensor {tuple(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _cache_struct(cache, device, dtype=None) -> FbKvCacheStruct:
+    """(k_pages, v_pages), each [pages, Hkv, page_size, D] -> the C struct."""
+    k, v = cache
+    if (k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.dtype not in _DTYPES
+            or not k.is_contiguous() or not v.is_contiguous() or k.device != device or v.device != device
+            or (dtype is not None and k.dtype != dtype)):
+        raise ValueError("cache: two contiguous [pages, Hkv, page_size, D] tensors of the heads' type and device")
+    pages, Hkv, page_size, D = k.shape
+    return FbKvCacheStruct(k=k.data_ptr(), v=v.data_ptr(), t=_DTYPES[k.dtype], pages=pages, page_size=page_size,
+                           Hkv=Hkv, D=D)
+
+
+def rope_frequencies(rot: int, theta: float = 10000.0, device="cuda") -> torch.Tensor:
+    """theta^(-2p / rot) for the rot/2 pairs of a rotation: float64, as fb_qk_norm_rope takes them."""
+    return float(theta) ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=device) / rot)
+
+
+def fb_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: Optional[torch.Tensor],
+                    inv_freq: Optional[torch.Tensor], q_weight: Optional[torch.Tensor] = None,
+                    k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, interleaved: bool = False,
+                    cache=None, slots: Optional[torch.Tensor] = None, out_dtype=None,
+                    q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                    v_out: Optional[torch.Tensor] = None, flags: int = 0):
+    """Norm and rotation of projected heads, and their write into a paged cache, in one pass.
+
+    q [T, Hq, D], k and v [T, Hkv, D] (f32/f16/bf16; rows may be strided, as slices of a fused projection);
+    pos int32 [T]; inv_freq float64 [rot/2] (None: no rotation); q_weight, k_weight float32 [D] (None: no norm).
+    interleaved: pairs are neighbouring elements, not the halves of the rotated part.  cache = (k_pages, v_pages),
+    [pages, Hkv, page_size, D] each, takes the keys and values at slots int32 [T] (slots outside are skipped).
+    Returns (q_out, k_out, v_out): q_out is made when not given; k_out and v_out are made only where there is no
+    cache.  Their type is out_dtype: by default the cache's, else a given output's, else the heads' (bf16 for
+    f32 heads).  The outputs may be the inputs (in place)."""
+    dev, (T, Hq, D), Hkv = q.device, q.shape, k.shape[1] if k.dim() == 3 else 0
+    ldq = _head_rows(q, "q")
+    ldk = _head_rows(k, "k", dev, (T, Hkv, D), q.dtype)
+    ldv = _head_rows(v, "v", dev, (T, Hkv, D), q.dtype)
+    given = next((t.dtype for t in (q_out, k_out, v_out) if t is not None), None)
+    dt = out_dtype or (cache[0].dtype if cache is not None else given) or (
+        q.dtype if q.dtype != torch.float32 else torch.bfloat16)
+    if dt not in _DTYPES:
+        raise ValueError("out_dtype: torch.float16 or torch.bfloat16")
+    q_out = torch.empty((T, Hq, D), dtype=dt, device=dev) if q_out is None else q_out
+    if cache is None:
+        k_out = torch.empty((T, Hkv, D), dtype=dt, device=dev) if k_out is None else k_out
+        v_out = torch.empty((T, Hkv, D), dtype=dt, device=dev) if v_out is None else v_out
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    if rot and pos is None:
+        raise ValueError("pos: int32 [T] where there is a rotation")
+    if (cache is None) != (slots is None):
+        raise ValueError("cache and slots go together")
+    hin = FbHeadsStruct(q.data_ptr(), k.data_ptr(), v.data_ptr(), _DTYPES[q.dtype], T, Hq, Hkv, D, ldq, ldk, ldv)
+    hout = FbHeadsStruct(q_out.data_ptr(), _ptr(k_out), _ptr(v_out), _DTYPES[dt], T, Hq, Hkv, D,
+                         _head_rows(q_out, "q_out", dev, (T, Hq, D), dt),
+                         0 if k_out is None else _head_rows(k_out, "k_out", dev, (T, Hkv, D), dt),
+                         0 if v_out is None else _head_rows(v_out, "v_out", dev, (T, Hkv, D), dt))
+    kv = None if cache is None else C.byref(_cache_struct(cache, dev, dt))
+    _check(_on(dev, lib().fb_qk_norm_rope, C.byref(hin), C.byref(hout), _flat(pos, "pos", torch.int32, (T,), dev),
+               _flat(inv_freq, "inv_freq", torch.float64, (rot // 2,), dev), rot,
+               _flat(q_weight, "q_weight", torch.float32, (D,), dev),
+               _flat(k_weight, "k_weight", torch.float32, (D,), dev), eps, kv,
+               _flat(slots, "slots", torch.int32, (T,), dev), flags | (FB_ROPE_NEIGHBOURS if interleaved else 0)),
+           "fb_qk_norm_rope")
+    return q_out, k_out, v_out
+
+
+def fb_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                   scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                   lse: Optional[torch.Tensor] = None, flags: int = 0) -> torch.Tensor:
+    """Causal attention of packed prompts: q [T, Hq, D], k and v [T, Hkv, D] (f16/bf16, D 64 or 128; rows may be
+    strided), sequence s being tokens cu_seqlens[s] .. cu_seqlens[s+1]-1 (int32 [n+1]) -> [T, Hq, D].  scale
+    defaults to D^-0.5; lse float32 [T, Hq] takes the logarithms of the softmax's sums.  Rows of no sequence keep
+    what `out` holds (unset memory when it is not given)."""
+    dev, (T, Hq, D), Hkv = q.device, q.shape, k.shape[1] if k.dim() == 3 else 0
+    h = FbHeadsStruct(q.data_ptr(), k.data_ptr(), v.data_ptr(), _DTYPES.get(q.dtype, -1), T, Hq, Hkv, D,
+                      _head_rows(q, "q"), _head_rows(k, "k", dev, (T, Hkv, D), q.dtype),
+                      _head_rows(v, "v", dev, (T, Hkv, D), q.dtype))
+    out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev) if out is None else out
+    n = cu_seqlens.numel() - 1
+    _check(_on(dev, lib().fb_attn_prompt, C.byref(h), _flat(cu_seqlens, "cu_seqlens", torch.int32, (n + 1,), dev), n,
+               D ** -0.5 if scale is None else scale, out.data_ptr(),
+               _head_rows(out, "out", dev, (T, Hq, D), q.dtype), _flat(lse, "lse", torch.float32, (T, Hq), dev),
+               flags), "fb_attn_prompt")
+    return out
+
+
+def fb_attn_tree_workspace_bytes(Hq: int, Hkv: int, D: int, max_draft: int = 1) -> int:
+    return lib().fb_attn_tree_workspace_bytes(Hq, Hkv, D, max_draft)
+
+
+def fb_attn_tree(q: torch.Tensor, cache, page_table: torch.Tensor, lens: torch.Tensor,
+                 cu_draft: Optional[torch.Tensor] = None, max_draft: int = 1, mask: Optional[torch.Tensor] = None,
+                 scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                 lse: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                 flags: int = 0) -> torch.Tensor:
+    """Attention of each sequence's newest tokens over the paged cache: q [T, Hq, D] of the cache's type, cache =
+    (k_pages, v_pages), page_table int32 [n, width], lens int32 [n] committed keys, cu_draft int32 [n+1] the
+    sequences' tokens in q (None: one each, T = n), at most max_draft <= 64 a sequence, whose own keys are in the
+    cache at positions lens[s] + j.  mask int64 [T]: bit j of a token's word lets it see drafted token j of its
+    sequence (None: a chain, j <= i).  Returns [T, Hq, D]; scale, out and lse as for fb_attn_prompt.  ws (uint8)
+    is made when not given."""
+    dev, (T, Hq, D) = q.device, q.shape
+    ldq = _head_rows(q, "q")
+    kv = _cache_struct(cache, dev, q.dtype)
+    if kv.D != D:
+        raise ValueError("cache: another head width than q's")
+    n = lens.numel()
+    if page_table.dim() != 2 or page_table.shape[0] != n or page_table.stride(1) != 1 or (
+            page_table.dtype != torch.int32) or page_table.device != dev:
+        raise ValueError("page_table: an int32 [n, width] tensor with unit column stride on q's device")
+    ld_table = page_table.stride(0) if n > 1 else page_table.shape[1]
+    out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev) if out is None else out
+    if ws is None:
+        ws = torch.empty(max(fb_attn_tree_workspace_bytes(Hq, kv.Hkv, D, max_draft), 16), dtype=torch.uint8,
+                         device=dev)
+    _check(_on(dev, lib().fb_attn_tree, q.data_ptr(), ldq, T, Hq, C.byref(kv), page_table.data_ptr(),
+               page_table.shape[1], ld_table,
+               _flat(lens, "lens", torch.int32, (n,), dev), _flat(cu_draft, "cu_draft", torch.int32, (n + 1,), dev),
+               n, max_draft, _flat(mask, "mask", torch.int64, (T,), dev), D ** -0.5 if scale is None else scale,
+               out.data_ptr(), _head_rows(out, "out", dev, (T, Hq, D), q.dtype),
+               _flat(lse, "lse", torch.float32, (T, Hq), dev), ws.data_ptr(), ws.numel() * ws.element_size(), flags),
+           "fb_attn_tree")
+    return out

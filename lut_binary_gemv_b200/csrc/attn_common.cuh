@@ -1,0 +1,65 @@
+// attn_common.cuh -- what the attention calls share: argument checks of
+// heads and caches, packing of value pairs, the programmatic-launch wait.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "fb_internal.cuh"
+
+namespace fb {
+
+constexpr int kMaxTokens = 1 << 24;
+constexpr int kMaxHeads = 1024;
+
+inline int log2_of(int v) {
+    int s = 0;
+    while ((1 << s) < v) ++s;
+    return s;
+}
+
+inline bool valid_heads(const fb_heads &h) {
+    return dtype_size(h.t) && h.T >= 1 && h.T <= kMaxTokens && h.Hq >= 1 && h.Hq <= kMaxHeads && h.Hkv >= 1 &&
+           h.Hq % h.Hkv == 0 && h.D >= 1 && h.D <= 65536 && h.ldq >= h.Hq * h.D && h.ldk >= h.Hkv * h.D &&
+           h.ldv >= h.Hkv * h.D;
+}
+
+inline bool valid_cache(const fb_kv_cache &c) {
+    return c.k && c.v && (c.t == FB_F16 || c.t == FB_BF16) && c.pages >= 1 && c.Hkv >= 1 && c.Hkv <= kMaxHeads &&
+           c.D >= 1 && c.D <= 65536 && c.page_size >= 1 && c.page_size <= 1024 &&
+           (c.page_size & (c.page_size - 1)) == 0 && (int64_t)c.pages * c.page_size < ((int64_t)1 << 31);
+}
+
+// Two fp32 values rounded to T, the first in the low half.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t v);
+template <>
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t v) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+}
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t v) {
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&v));
+}
+
+// Programmatic dependent launch: returns once the previous kernel of the
+// stream has completed (at once for an ordinary launch).
+__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+}  // namespace fb

@@ -1,0 +1,137 @@
+"""Host-side checks of the attention calls (no GPU needed): every refusal of
+the C ABI comes back before anything is enqueued, and the binding refuses
+what it cannot describe to the library."""
+
+import ctypes as C
+import math
+
+import pytest
+import torch
+
+import lut_binary_gemv_b200 as fb
+from lut_binary_gemv_b200 import build as fb_build
+
+OK, INVALID, UNSUPPORTED, MISALIGNED, WORKSPACE, CUDA = range(6)
+FAKE = 0x10000   # aligned and never dereferenced by a call that is refused
+F32, F16, BF16 = 0, 1, 2
+
+
+@pytest.fixture(scope="module")
+def L():
+    fb_build.build()
+    return fb.lib()
+
+
+def heads(**over):
+    h = dict(q=FAKE, k=FAKE, v=FAKE, t=BF16, T=4, Hq=8, Hkv=2, D=128, ldq=1024, ldk=256, ldv=256)
+    h.update(over)
+    return fb.FbHeadsStruct(**h)
+
+
+def kv_cache(**over):
+    c = dict(k=FAKE, v=FAKE, t=BF16, pages=10, page_size=16, Hkv=2, D=128)
+    c.update(over)
+    return fb.FbKvCacheStruct(**c)
+
+
+def rope(L, hin=None, hout=None, pos=FAKE, inv=FAKE, rot=128, wq=FAKE, wk=FAKE, eps=1e-6, cache=True, slots=FAKE,
+         flags=0):
+    hin, hout = hin or heads(), hout or heads()
+    kv = kv_cache() if cache is True else cache
+    return L.fb_qk_norm_rope(C.byref(hin), C.byref(hout), pos, inv, rot, wq, wk, eps,
+                             None if kv is None else C.byref(kv), slots, flags, None)
+
+
+@pytest.mark.parametrize("args,status", [
+    (dict(hin=heads(q=None)), INVALID), (dict(hin=heads(k=None)), INVALID), (dict(hin=heads(v=None)), INVALID),
+    (dict(hin=heads(T=0)), INVALID), (dict(hin=heads(T=(1 << 24) + 1)), INVALID), (dict(hin=heads(t=7)), INVALID),
+    (dict(hin=heads(Hkv=3)), INVALID), (dict(hin=heads(Hkv=0)), INVALID), (dict(hin=heads(Hq=2000)), INVALID),
+    (dict(hin=heads(ldq=1016)), INVALID), (dict(hin=heads(ldk=128)), INVALID), (dict(hin=heads(ldv=0)), INVALID),
+    (dict(hout=heads(T=5)), INVALID), (dict(hout=heads(Hq=4)), INVALID), (dict(hout=heads(D=64)), INVALID),
+    (dict(hout=heads(ldq=1000)), INVALID), (dict(hout=heads(ldk=8)), INVALID),
+    (dict(pos=None), INVALID), (dict(inv=None), INVALID), (dict(rot=-16), INVALID), (dict(rot=144), INVALID),
+    (dict(eps=-1.0), INVALID), (dict(eps=math.nan), INVALID), (dict(eps=math.inf), INVALID),
+    (dict(slots=None), INVALID), (dict(cache=kv_cache(Hkv=1)), INVALID), (dict(cache=kv_cache(D=64)), INVALID),
+    (dict(cache=kv_cache(t=F16)), INVALID), (dict(cache=kv_cache(page_size=24)), INVALID),
+    (dict(cache=kv_cache(page_size=2048)), INVALID), (dict(cache=kv_cache(pages=0)), INVALID),
+    (dict(cache=kv_cache(pages=1 << 27)), INVALID), (dict(cache=kv_cache(k=None)), INVALID),
+    (dict(flags=2), INVALID), (dict(flags=0x20), INVALID),
+    (dict(hout=heads(t=F32), cache=None, slots=None), UNSUPPORTED), (dict(rot=24), UNSUPPORTED),
+    (dict(hin=heads(D=120, ldq=960, ldk=240, ldv=240), hout=heads(D=120, ldq=960, ldk=240, ldv=240), rot=112,
+          cache=None), UNSUPPORTED),
+    (dict(hin=heads(D=272, ldq=2176, ldk=544, ldv=544), hout=heads(D=272, ldq=2176, ldk=544, ldv=544),
+          cache=None), UNSUPPORTED),
+    (dict(hin=heads(q=FAKE + 8)), MISALIGNED), (dict(hin=heads(ldk=260)), MISALIGNED),
+    (dict(hout=heads(v=FAKE + 2)), MISALIGNED), (dict(hout=heads(ldq=1028)), MISALIGNED),
+    (dict(pos=FAKE + 2), MISALIGNED), (dict(inv=FAKE + 4), MISALIGNED), (dict(wq=FAKE + 1), MISALIGNED),
+    (dict(slots=FAKE + 2), MISALIGNED), (dict(cache=kv_cache(v=FAKE + 8)), MISALIGNED),
+])
+def test_rope_refusals(L, args, status):
+    assert rope(L, **args) == status
+
+
+def prompt(L, h=None, cu=FAKE, n=2, scale=0.1, out=FAKE, ldo=1024, lse=FAKE, flags=0):
+    h = h or heads()
+    return L.fb_attn_prompt(C.byref(h), cu, n, scale, out, ldo, lse, flags, None)
+
+
+@pytest.mark.parametrize("args,status", [
+    (dict(h=heads(q=None)), INVALID), (dict(h=heads(k=None)), INVALID), (dict(h=heads(v=None)), INVALID),
+    (dict(h=heads(T=0)), INVALID), (dict(h=heads(Hkv=5)), INVALID), (dict(h=heads(ldq=512)), INVALID),
+    (dict(cu=None), INVALID), (dict(n=0), INVALID), (dict(out=None), INVALID), (dict(ldo=1016), INVALID),
+    (dict(scale=0.0), INVALID), (dict(scale=-0.1), INVALID), (dict(scale=math.nan), INVALID),
+    (dict(scale=math.inf), INVALID), (dict(flags=2), INVALID), (dict(flags=0x10), INVALID),
+    (dict(h=heads(t=F32)), UNSUPPORTED), (dict(h=heads(D=96)), UNSUPPORTED),
+    (dict(h=heads(q=FAKE + 8)), MISALIGNED), (dict(h=heads(ldv=260)), MISALIGNED), (dict(out=FAKE + 8), MISALIGNED),
+    (dict(ldo=1028), MISALIGNED), (dict(cu=FAKE + 1), MISALIGNED), (dict(lse=FAKE + 2), MISALIGNED),
+])
+def test_prompt_refusals(L, args, status):
+    assert prompt(L, **args) == status
+
+
+def tree(L, q=FAKE, ldq=1024, T=4, Hq=8, cache=None, table=FAKE, width=8, ld=8, lens=FAKE, cu=FAKE, n=2, most=3,
+         mask=FAKE, scale=0.1, out=FAKE, ldo=1024, lse=FAKE, ws=FAKE, ws_bytes=1 << 30, flags=0):
+    kv = cache or kv_cache()
+    return L.fb_attn_tree(q, ldq, T, Hq, C.byref(kv), table, width, ld, lens, cu, n, most, mask, scale, out, ldo, lse,
+                          ws, ws_bytes, flags, None)
+
+
+@pytest.mark.parametrize("args,status", [
+    (dict(q=None), INVALID), (dict(table=None), INVALID), (dict(lens=None), INVALID), (dict(out=None), INVALID),
+    (dict(T=0), INVALID), (dict(Hq=7), INVALID), (dict(Hq=0), INVALID), (dict(n=0), INVALID), (dict(n=65537), INVALID),
+    (dict(cu=None), INVALID), (dict(most=0), INVALID), (dict(most=65), INVALID), (dict(width=0), INVALID),
+    (dict(ld=7), INVALID), (dict(ldq=1016), INVALID), (dict(ldo=8), INVALID), (dict(scale=0.0), INVALID),
+    (dict(scale=math.nan), INVALID), (dict(flags=2), INVALID), (dict(cache=kv_cache(t=F32)), INVALID),
+    (dict(cache=kv_cache(page_size=0)), INVALID), (dict(cache=kv_cache(v=None)), INVALID),
+    (dict(cache=kv_cache(D=96), ldq=1024), UNSUPPORTED),
+    (dict(q=FAKE + 8), MISALIGNED), (dict(out=FAKE + 4), MISALIGNED), (dict(ldq=1028), MISALIGNED),
+    (dict(table=FAKE + 2), MISALIGNED), (dict(lens=FAKE + 1), MISALIGNED), (dict(cu=FAKE + 2), MISALIGNED),
+    (dict(mask=FAKE + 4), MISALIGNED), (dict(lse=FAKE + 1), MISALIGNED),
+    (dict(ws=None), WORKSPACE), (dict(ws=FAKE + 8), WORKSPACE), (dict(ws_bytes=0), WORKSPACE),
+])
+def test_tree_refusals(L, args, status):
+    assert tree(L, **args) == status
+
+
+def test_tree_workspace_bytes(L):
+    assert L.fb_attn_tree_workspace_bytes(64, 8, 128, 1) > 0
+    for bad in [(0, 1, 128, 1), (8, 3, 128, 1), (8, 0, 128, 1), (8, 8, 96, 1), (8, 8, 64, 0), (8, 8, 64, 65),
+                (2048, 8, 64, 1)]:
+        assert L.fb_attn_tree_workspace_bytes(*bad) == 0
+
+
+def test_binding_refuses_what_is_not_on_the_gpu_or_shaped_otherwise():
+    q, k = torch.zeros(4, 8, 128, dtype=torch.bfloat16), torch.zeros(4, 2, 128, dtype=torch.bfloat16)
+    cu = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        fb.fb_attn_prompt(q, k, k, cu)
+    with pytest.raises(ValueError):
+        fb.fb_qk_norm_rope(q, k, k, None, None)
+    with pytest.raises(ValueError):
+        fb.fb_attn_tree(q, (k, k), cu[None], cu)
+
+
+def test_rope_frequencies():
+    f = fb.rope_frequencies(8, 10000.0, device="cpu")
+    assert f.dtype == torch.float64 and torch.allclose(f, torch.tensor([1.0, 0.1, 0.01, 0.001], dtype=torch.float64),
+                                                       rtol=1e-14)

@@ -4,13 +4,35 @@
 //   out_i = sum_j p_ij v_j over the committed keys and the drafted keys whose
 //   bit is set in the token's mask, p the softmax of scale q_i.k_j.
 //
-// One warp a row: right for every case, bound by re-reading the keys for
-// every row and by one warp's walk along a long cache.
+// A key and its value are read once for the rows that share them (the drafted
+// tokens times the query heads of a key head), so for few rows the kernel is
+// bound by HBM and everything serves the stream of keys:
+//
+//  * The work is the list of (sequence, key head, row tile, tile of 64 keys),
+//    cut into one equal run of key tiles for each resident CTA, whatever the
+//    lengths: a long sequence spreads over many CTAs and a CTA takes many short
+//    ones.  Each CTA finds its run from the lengths on the device.  A sequence
+//    cut by a run's end leaves its running maximum, sum and unnormalised output
+//    in the workspace (a CTA has at most two such pieces, its first and its
+//    last), and join_kernel joins them in order, so results do not depend on
+//    timing.
+//  * Of a tile, each warp owns 16 keys for all rows (up to 32 of them): it
+//    loads them itself with asynchronous copies two tiles ahead, across the
+//    ends of sequences, and needs no CTA barrier until the piece ends.  From 33
+//    rows on two warps share 32 keys and split 64 rows.
+//  * Scores and outputs are m16n8k16 products with fp32 accumulators; the
+//    weights stay in registers between the two.
+//
+// A tile that reaches into the drafted keys may hold infinities or NaN that
+// some rows must not see, and a weight of zero does not stop them: such values
+// are added to the rows that see them and cleared before the product.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "attn_common.cuh"
 #include "fb_internal.cuh"
@@ -19,6 +41,10 @@ namespace fb {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr int kTileKeys = 64;      // keys of a tile, 16 loaded by each warp
+constexpr int kCtasPerSm = 2;
+constexpr int kMinTiles = 2;       // key tiles of a run, at least
 
 __device__ unsigned int g_attn_errors;
 
@@ -28,71 +54,534 @@ struct TreeArgs {
     float *lse;
     const int32_t *table, *lens, *cu;
     const uint64_t *mask;
-    int n, T, Hq, Hkv, ldq, ldo, table_width, ld_table, max_draft, pages, page_shift;
-    float scale;
+    float *part, *part_ml;
+    int4 *records;
+    int n, T, Hkv, group, ldq, ldo, table_width, ld_table, max_draft, pages, page_shift;
+    float scale_log2;
 };
 
-template <typename E, int D>
-__global__ void __launch_bounds__(kThreads) tree_rows_kernel(const TreeArgs a) {
-    wait_for_previous_kernel();
-    const int64_t row = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
-    const int lane = threadIdx.x % 32, i = (int)(row / a.Hq), h = (int)(row % a.Hq);
-    if (i >= a.T) return;
-    int seq = i, first = i, m_s = 1;
+// One sequence as the kernels see it: its tokens, its keys and its work.
+struct Seq {
+    int first, m, len, tiles, row_tiles;
+    bool too_many;
+};
+
+template <int ROWS>
+__device__ __forceinline__ Seq sequence(const TreeArgs &a, int s) {
+    Seq q;
+    int first = s, end = s + 1;
     if (a.cu) {
-        int lo = 0, hi = a.n;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) / 2;
-            if (mid < a.n && a.cu[mid] <= i) lo = mid;
-            else hi = mid - 1;
-        }
-        seq = lo, first = max(a.cu[lo], 0);
-        const int end = min(a.cu[lo + 1], a.T);
-        if (i < first || i >= end) return;
-        m_s = end - first;
-        if (m_s > a.max_draft) {
-            m_s = a.max_draft;
-            if (lane == 0) atomicOr(&g_attn_errors, 2u);
-            if (i - first >= m_s) return;
-        }
+        first = min(max(a.cu[s], 0), a.T);
+        end = min(max(a.cu[s + 1], first), a.T);
     }
-    const int len = max(a.lens[seq], 0), d = i - first;
-    const uint64_t bits = a.mask ? a.mask[i] : ~0ull >> (63 - d);
-    constexpr int P = D / 64;
-    const E *q = (const E *)a.q + (size_t)i * a.ldq + (size_t)h * D;
-    const int hk = h / (a.Hq / a.Hkv);
-    float2 qv[P], o[P] = {};
-    for (int p = 0; p < P; ++p) qv[p] = unpack2<E>(((const uint32_t *)q)[32 * p + lane]);
-    float m = -INFINITY, l = 0.0f;
-    for (int64_t j = 0; j < (int64_t)len + m_s; ++j) {
-        if (j >= len && !(bits >> (j - len) & 1)) continue;
-        const int64_t slot = j >> a.page_shift;
-        const int page = slot < a.table_width ? a.table[(size_t)seq * a.ld_table + slot] : -1;
-        if (page < 0 || page >= a.pages) {
-            if (lane == 0) atomicOr(&g_attn_errors, 2u);
-            l = NAN;
-            break;
-        }
-        const size_t at = ((((size_t)page * a.Hkv + hk) << a.page_shift) + (j - (slot << a.page_shift))) * D;
-        const uint32_t *k = (const uint32_t *)((const E *)a.kc + at), *v = (const uint32_t *)((const E *)a.vc + at);
-        float s = 0.0f;
-        for (int p = 0; p < P; ++p) {
-            const float2 kv = unpack2<E>(k[32 * p + lane]);
-            s = fmaf(qv[p].x, kv.x, fmaf(qv[p].y, kv.y, s));
-        }
-        for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(~0u, s, x);
-        s *= a.scale;
-        const float mn = fmaxf(m, s), f = m == -INFINITY ? 0.0f : expf(m - mn), w = expf(s - mn);
-        l = l * f + w, m = mn;
-        for (int p = 0; p < P; ++p) {
-            const float2 vv = unpack2<E>(v[32 * p + lane]);
-            o[p].x = o[p].x * f + w * vv.x, o[p].y = o[p].y * f + w * vv.y;
-        }
+    q.first = first;
+    q.too_many = end - first > a.max_draft;
+    q.m = min(end - first, a.max_draft);
+    // more committed keys than the table has room for: one beyond it is enough to make every row NaN
+    const int64_t room = min(((int64_t)a.table_width << a.page_shift) + 1, (int64_t)INT32_MAX - 256);
+    q.len = (int)min((int64_t)max(a.lens[s], 0), room);
+    q.tiles = max(1, (q.len + q.m + kTileKeys - 1) / kTileKeys);
+    q.row_tiles = (q.m * a.group + ROWS - 1) / ROWS;
+    return q;
+}
+
+// A place in the list of key tiles.
+struct Cursor {
+    Seq q;
+    int s, item, kt;   // item = key head * row tiles + row tile
+};
+
+template <int ROWS>
+__device__ __forceinline__ void step(const TreeArgs &a, Cursor &c) {
+    if (++c.kt < c.q.tiles) return;
+    c.kt = 0;
+    if (++c.item < c.q.row_tiles * a.Hkv) return;
+    c.item = 0;
+    do {
+        if (++c.s >= a.n) return;
+        c.q = sequence<ROWS>(a, c.s);
+    } while (c.q.row_tiles == 0);
+}
+
+__device__ __forceinline__ uint32_t smem_address(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+template <typename E>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (std::is_same_v<E, __half>)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Byte offset of the 16-byte chunk of a row in a tile of 16-bit rows: the
+// chunk index is turned by the row, so that the eight rows of a matrix load
+// lie in eight different groups of banks.
+template <int D>
+__device__ __forceinline__ int chunk_at(int row, int chunk) {
+    return row * (D * 2) + ((chunk ^ (row & 7)) << 4);
+}
+
+template <typename E>
+__device__ __forceinline__ bool not_finite(uint32_t pair) {
+    constexpr uint32_t e = std::is_same_v<E, __half> ? 0x7C00u : 0x7F80u;
+    return (pair & e) == e || (pair >> 16 & e) == e;
+}
+template <typename E>
+__device__ __forceinline__ uint32_t finite_part(uint32_t pair) {
+    constexpr uint32_t e = std::is_same_v<E, __half> ? 0x7C00u : 0x7F80u;
+    if ((pair & e) == e) pair &= 0xFFFF0000u;
+    if ((pair >> 16 & e) == e) pair &= 0x0000FFFFu;
+    return pair;
+}
+
+template <int D>
+constexpr int kStages = 384 / D;   // 96 KB of tiles in flight a CTA, two CTAs an SM
+template <int D>
+constexpr int kStageBytes = kTileKeys * D * 2 * 2;
+
+template <int D, int WR, int MT>
+constexpr int tree_smem_bytes() {
+    return kStages<D> * kStageBytes<D> + WR * MT * 16 * D * 2;
+}
+
+// WR row warps times WK key warps; MT row tiles of 16 a warp.
+template <typename E, int D, int WR, int WK, int MT>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const TreeArgs a) {
+    static_assert(WR * WK == kWarps, "four warps");
+    constexpr int ROWS = WR * MT * 16;
+    constexpr int KW = kTileKeys / WK;      // keys a warp multiplies
+    constexpr int NT = KW / 8;              // 8-key columns of its scores
+    constexpr int CH = D / 8;               // 16-byte chunks of a row
+    constexpr int S = kStages<D>;
+    constexpr int kHalfStage = kTileKeys * D * 2;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ uint64_t s_mask[ROWS];
+    __shared__ float s_ml[2][kWarps][MT * 16];
+
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int wr = warp % WR, wk = warp / WR;
+    const uint32_t stages = smem_address(smem), q_at = stages + S * kStageBytes<D>;
+
+    wait_for_previous_kernel();
+
+    // ---- this CTA's run of key tiles -----------------------------------------
+    int64_t total = 0;
+    for (int s = lane; s < a.n; s += 32) {
+        const Seq q = sequence<ROWS>(a, s);
+        total += (int64_t)q.row_tiles * a.Hkv * q.tiles;
+        if (q.too_many && blockIdx.x == 0 && warp == 0) atomicOr(&g_attn_errors, 2u);
     }
-    const float r = l == 0.0f ? 0.0f : 1.0f / l;
-    uint32_t *out = (uint32_t *)((E *)a.out + (size_t)i * a.ldo + (size_t)h * D);
-    for (int p = 0; p < P; ++p) out[32 * p + lane] = pack2<E>(o[p].x * r, o[p].y * r);
-    if (a.lse && lane == 0) a.lse[(size_t)i * a.Hq + h] = l == 0.0f ? -INFINITY : m + logf(l);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) total += __shfl_xor_sync(~0u, total, x);
+    const int64_t run = max((total + gridDim.x - 1) / gridDim.x, (int64_t)kMinTiles);
+    const int64_t begin = run * blockIdx.x;
+    const int64_t mine = min(run, total - begin);
+    int64_t left = mine;
+    if (tid == 0) a.records[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (left <= 0) return;
+
+    Cursor at;
+    {
+        int64_t before = 0;
+        int base = 0;
+        for (;; base += 32) {
+            int64_t w = 0;
+            if (base + lane < a.n) {
+                const Seq q = sequence<ROWS>(a, base + lane);
+                w = (int64_t)q.row_tiles * a.Hkv * q.tiles;
+            }
+            int64_t upto = w;
+#pragma unroll
+            for (int x = 1; x < 32; x <<= 1) {
+                const int64_t y = __shfl_up_sync(~0u, upto, x);
+                if (lane >= x) upto += y;
+            }
+            const unsigned past = __ballot_sync(~0u, before + upto > begin);
+            if (past) {
+                const int l = __ffs(past) - 1;
+                at.s = base + l;
+                before += __shfl_sync(~0u, upto - w, l);
+                break;
+            }
+            before += __shfl_sync(~0u, upto, 31);
+        }
+        at.q = sequence<ROWS>(a, at.s);
+        at.item = (int)((begin - before) / at.q.tiles);
+        at.kt = (int)((begin - before) % at.q.tiles);
+    }
+
+    // ---- loading: each warp brings in keys 16 warp .. 16 warp + 15 of a tile ----
+    Cursor ahead = at;
+    int64_t to_load = left;
+    int load_stage = 0;
+    auto load_tile = [&]() {
+        if (to_load > 0) {
+            const int hk = ahead.item / ahead.q.row_tiles;
+            // lane r (and r + 16) finds the row of key r: its element offset, -1 behind the keys, -2 on a bad page
+            int64_t off = -1;
+            const int p = ahead.kt * kTileKeys + 16 * warp + lane % 16;
+            if (p < ahead.q.len + ahead.q.m) {
+                const int slot = p >> a.page_shift;
+                const int page = slot < a.table_width ? a.table[(size_t)ahead.s * a.ld_table + slot] : -1;
+                if (page >= 0 && page < a.pages) {
+                    off = ((((int64_t)page * a.Hkv + hk) << a.page_shift) + (p - (slot << a.page_shift))) * D;
+                } else {
+                    off = -2;
+                    atomicOr(&g_attn_errors, 2u);
+                }
+            }
+            const uint32_t k_at = stages + load_stage * kStageBytes<D>, v_at = k_at + kHalfStage;
+            const int chunk = lane % CH;
+#pragma unroll
+            for (int i = 0; i < 16 * CH / 32; ++i) {
+                const int r = i * (32 / CH) + lane / CH;
+                const int64_t o = __shfl_sync(~0u, off, r);
+                const int d = chunk_at<D>(16 * warp + r, chunk);
+                if (o == -2) {
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(k_at + d), "r"(0x7FFF7FFFu) : "memory");
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(v_at + d), "r"(0x7FFF7FFFu) : "memory");
+                } else {
+                    const int64_t e = o < 0 ? 0 : o + chunk * 8;
+                    copy16(k_at + d, (const E *)a.kc + e, o >= 0);
+                    copy16(v_at + d, (const E *)a.vc + e, o >= 0);
+                }
+            }
+            --to_load;
+            if (to_load > 0) step<ROWS>(a, ahead);
+        }
+        copies_close();
+        load_stage = load_stage + 1 == S ? 0 : load_stage + 1;
+    };
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) load_tile();
+
+    // ---- the pieces -------------------------------------------------------------
+    int stage = 0, last_stage = 0;
+    while (left > 0) {
+        const Seq q = at.q;
+        const int hk = at.item / q.row_tiles, rt = at.item % q.row_tiles;
+        const int kt0 = at.kt, kt1 = (int)min((int64_t)q.tiles, at.kt + left);
+        const int rows = min(ROWS, q.m * a.group - rt * ROWS);
+
+        // the rows' queries and masks (row r: token r / group, head r % group of the key head's)
+        __syncthreads();
+        for (int i = tid; i < ROWS * CH; i += kThreads) {
+            const int r = i / CH, c = i % CH, rr = rt * ROWS + r;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (r < rows) {
+                const int token = q.first + rr / a.group, h = hk * a.group + rr % a.group;
+                v = *reinterpret_cast<const uint4 *>((const E *)a.q + (size_t)token * a.ldq + (size_t)h * D + c * 8);
+            }
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(q_at + chunk_at<D>(r, c)), "r"(v.x), "r"(v.y),
+                         "r"(v.z), "r"(v.w)
+                         : "memory");
+        }
+        if (tid < ROWS) {
+            const int i = (rt * ROWS + tid) / a.group;
+            uint64_t bits = 0;
+            if (tid < rows) bits = a.mask ? a.mask[q.first + i] : ~0ull >> (63 - i);
+            s_mask[tid] = q.m < 64 ? bits & ((1ull << q.m) - 1) : bits;
+        }
+        __syncthreads();
+
+        float o[MT][D / 8][4] = {};
+        float m[MT][2], l[MT][2];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) m[t][0] = m[t][1] = -INFINITY, l[t][0] = l[t][1] = 0.0f;
+
+        for (int kt = kt0; kt < kt1; ++kt) {
+            copies_wait<S - 2>();
+            if (WK == kWarps) __syncwarp();
+            else __syncthreads();
+            load_tile();   // into the place of the tile before, which its readers have left
+            const uint32_t k_at = stages + stage * kStageBytes<D>, v_at = k_at + kHalfStage;
+            const int key0 = wk * KW;
+
+            float s[MT][NT][4] = {};
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+                uint32_t qa[MT][4];
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+                    ldmatrix4(qa[t], q_at + chunk_at<D>((wr * MT + t) * 16 + lane % 16, 2 * d + lane / 16));
+#pragma unroll
+                for (int j = 0; j < NT; j += 2) {
+                    uint32_t kb[4];
+                    ldmatrix4(kb, k_at + chunk_at<D>(key0 + 8 * j + lane % 8 + (lane / 16) * 8, 2 * d + (lane / 8) % 2));
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) mma<E>(s[t][j], qa[t], kb[0], kb[1]), mma<E>(s[t][j + 1], qa[t], kb[2], kb[3]);
+                }
+            }
+
+            const int tile_key = kt * kTileKeys;
+            const bool partly = tile_key + kTileKeys > q.len;   // some keys are drafted, or behind the last
+            if (partly) {
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint64_t bits = s_mask[(wr * MT + t) * 16 + half * 8 + lane / 4];
+#pragma unroll
+                        for (int j = 0; j < NT; ++j)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int dj = tile_key + key0 + 8 * j + 2 * (lane % 4) + e - q.len;
+                                const bool sees = dj < 0 || (dj < 64 && (bits >> dj & 1));
+                                if (!sees) s[t][j][2 * half + e] = -INFINITY;
+                            }
+                    }
+            }
+
+            uint32_t pa[MT][NT / 2][4];
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) top = fmaxf(top, fmaxf(s[t][j][2 * half], s[t][j][2 * half + 1]));
+                    top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+                    const float mn = fmaxf(m[t][half], top * a.scale_log2);
+                    const float ref = mn == -INFINITY ? 0.0f : mn;
+                    const float f = exp2_approx(m[t][half] - ref);
+                    m[t][half] = mn;
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        const float p0 = exp2_approx(fmaf(s[t][j][2 * half], a.scale_log2, -ref));
+                        const float p1 = exp2_approx(fmaf(s[t][j][2 * half + 1], a.scale_log2, -ref));
+                        sum += p0 + p1;
+                        pa[t][j / 2][(j % 2) * 2 + half] = pack2<E>(p0, p1);
+                    }
+                    l[t][half] = l[t][half] * f + sum;
+#pragma unroll
+                    for (int j = 0; j < D / 8; ++j) o[t][j][2 * half] *= f, o[t][j][2 * half + 1] *= f;
+                }
+
+            if (partly) {
+                // values that are not finite: scanned by the warp that loaded them
+                bool odd = false;
+                for (int i = lane; i < 16 * CH; i += 32) {
+                    const uint32_t x = v_at + chunk_at<D>(16 * warp + i / CH, i % CH);
+                    uint4 v;
+                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(x) : "memory");
+                    odd |= not_finite<E>(v.x) || not_finite<E>(v.y) || not_finite<E>(v.z) || not_finite<E>(v.w);
+                }
+                odd = WK == kWarps ? __any_sync(~0u, odd) : __syncthreads_or(odd);
+                if (odd) {
+                    for (int kk = 0; kk < KW; ++kk) {
+                        const int dj = tile_key + key0 + kk - q.len;
+#pragma unroll
+                        for (int t = 0; t < MT; ++t)
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                const uint64_t bits = s_mask[(wr * MT + t) * 16 + half * 8 + lane / 4];
+                                if (!(dj < 0 || (dj < 64 && (bits >> dj & 1)))) continue;
+#pragma unroll
+                                for (int j = 0; j < D / 8; ++j) {
+                                    uint32_t v;
+                                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(v_at + chunk_at<D>(key0 + kk, j) + 4 * (lane % 4)) : "memory");
+                                    if (not_finite<E>(v)) {
+                                        const float2 f = unpack2<E>(v ^ finite_part<E>(v));
+                                        o[t][j][2 * half] += f.x, o[t][j][2 * half + 1] += f.y;
+                                    }
+                                }
+                            }
+                    }
+                    if (WK == kWarps) __syncwarp();
+                    else __syncthreads();
+                    for (int i = lane; i < 16 * CH * 4; i += 32) {
+                        const uint32_t x = v_at + chunk_at<D>(16 * warp + i / (4 * CH), i / 4 % CH) + 4 * (i % 4);
+                        uint32_t v;
+                        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(x) : "memory");
+                        if (not_finite<E>(v)) asm volatile("st.shared.b32 [%0], %1;" ::"r"(x), "r"(finite_part<E>(v)) : "memory");
+                    }
+                    if (WK == kWarps) __syncwarp();
+                    else __syncthreads();
+                }
+            }
+
+#pragma unroll
+            for (int c = 0; c < NT / 2; ++c)
+#pragma unroll
+                for (int d = 0; d < D / 16; ++d) {
+                    uint32_t vb[4];
+                    ldmatrix4_trans(vb, v_at + chunk_at<D>(key0 + 16 * c + lane % 16, 2 * d + lane / 16));
+#pragma unroll
+                    for (int t = 0; t < MT; ++t)
+                        mma<E>(o[t][2 * d], pa[t][c], vb[0], vb[1]), mma<E>(o[t][2 * d + 1], pa[t][c], vb[2], vb[3]);
+                }
+
+            last_stage = stage;
+            stage = stage + 1 == S ? 0 : stage + 1;
+            step<ROWS>(a, at);
+        }
+
+        // ---- join the key warps through the last tile's place (free until the next tile is
+        // asked for, behind the next piece's first barrier): 16 rows a warp at a time ----
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                l[t][half] += __shfl_xor_sync(~0u, l[t][half], 1);
+                l[t][half] += __shfl_xor_sync(~0u, l[t][half], 2);
+                if (lane % 4 == 0) {
+                    s_ml[0][warp][t * 16 + half * 8 + lane / 4] = m[t][half];
+                    s_ml[1][warp][t * 16 + half * 8 + lane / 4] = l[t][half];
+                }
+            }
+        const bool whole = kt0 == 0 && kt1 == q.tiles;
+        const size_t piece = 2 * (size_t)blockIdx.x + (kt0 == 0 ? 1 : 0);
+        constexpr int kSlice = 16 * D * 4;
+        static_assert(kSlice * kWarps == kStageBytes<D>, "a warp's 16 rows in fp32 fill its share of a tile's place");
+        uint8_t *join = smem + last_stage * kStageBytes<D>;
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            __syncthreads();   // all warps are done with the tile (or with the rows before)
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int j = 0; j < D / 8; ++j) {
+                    const int r = half * 8 + lane / 4, c = 2 * j + (lane % 4) / 2;
+                    *reinterpret_cast<float2 *>(join + warp * kSlice + r * D * 4 + ((c ^ (r & 7) * 2) << 4) + (lane % 2) * 8) =
+                        make_float2(o[t][j][2 * half], o[t][j][2 * half + 1]);
+                }
+            __syncthreads();
+            // warp (wr, wk) takes the columns wk of WK of its row warp's 16 rows, four at a time
+            constexpr int CW = D / 4 / WK;                     // chunks of four columns a warp joins
+            for (int i = lane; i < 16 * CW; i += 32) {
+                const int r = i / CW, c = wk * CW + i % CW, row = (wr * MT + t) * 16 + r;
+                if (row >= rows) continue;
+                float top = -INFINITY;
+#pragma unroll
+                for (int x = 0; x < WK; ++x) top = fmaxf(top, s_ml[0][x * WR + wr][t * 16 + r]);
+                const float ref = top == -INFINITY ? 0.0f : top;
+                float4 y = make_float4(0, 0, 0, 0);
+                float sum = 0.0f;
+#pragma unroll
+                for (int x = 0; x < WK; ++x) {
+                    const int w = x * WR + wr;
+                    const float f = exp2_approx(s_ml[0][w][t * 16 + r] - ref);
+                    const float4 v = *reinterpret_cast<const float4 *>(join + w * kSlice + r * D * 4 + ((c ^ (r & 7) * 2) << 4));
+                    sum = fmaf(f, s_ml[1][w][t * 16 + r], sum);
+                    y.x = fmaf(f, v.x, y.x), y.y = fmaf(f, v.y, y.y), y.z = fmaf(f, v.z, y.z), y.w = fmaf(f, v.w, y.w);
+                }
+                if (whole) {
+                    const int rr = rt * ROWS + row, token = q.first + rr / a.group, h = hk * a.group + rr % a.group;
+                    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                    uint2 packed;
+                    packed.x = pack2<E>(y.x * inv, y.y * inv), packed.y = pack2<E>(y.z * inv, y.w * inv);
+                    *reinterpret_cast<uint2 *>((E *)a.out + (size_t)token * a.ldo + (size_t)h * D + 4 * c) = packed;
+                    if (a.lse && c == 0)
+                        a.lse[(size_t)token * a.Hkv * a.group + h] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.69314718056f;
+                } else {
+                    *reinterpret_cast<float4 *>(a.part + (piece * ROWS + row) * D + 4 * c) = y;
+                    if (c == 0) *reinterpret_cast<float2 *>(a.part_ml + (piece * ROWS + row) * 2) = make_float2(top, sum);
+                }
+            }
+        }
+        // the CTA where a cut sequence begins tells the join where it lies and in which CTA it ends
+        if (!whole && kt0 == 0 && tid == 0) {
+            const int64_t end = begin + (mine - left) + q.tiles;
+            a.records[blockIdx.x] = make_int4((int)((end - 1) / run) + 1, q.first, hk * q.row_tiles + rt, rows | q.row_tiles << 16);
+        }
+        left -= kt1 - kt0;
+    }
+    copies_wait<0>();
+}
+
+// Joins the pieces of the cut sequences: block x the one that begins in CTA x,
+// four rows (eight of 64 elements) a block; the pieces in order.
+template <typename E, int D, int ROWS>
+__global__ void __launch_bounds__(kThreads) join_kernel(const TreeArgs a) {
+    wait_for_previous_kernel();
+    const int4 rec = a.records[blockIdx.x];
+    const int row_tiles = rec.w >> 16, rows = rec.w & 0xFFFF;
+    const int row = blockIdx.y * (kThreads * 4 / D) + threadIdx.x / (D / 4), c = threadIdx.x % (D / 4);
+    if (rec.x == 0 || row >= rows) return;
+    const int first = blockIdx.x, last = rec.x - 1;
+    float top = -INFINITY, sum = 0.0f;
+    float4 y = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+    for (int x = first; x <= last; ++x) {
+        const size_t at = (2 * (size_t)x + (x == first ? 1 : 0)) * ROWS + row;
+        const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + at * 2);
+        const float4 v = *reinterpret_cast<const float4 *>(a.part + at * D + 4 * c);
+        const float mn = fmaxf(top, ml.x), ref = mn == -INFINITY ? 0.0f : mn;
+        const float f = exp2_approx(top - ref), g = exp2_approx(ml.x - ref);
+        top = mn;
+        sum = sum * f + ml.y * g;
+        y.x = y.x * f + v.x * g, y.y = y.y * f + v.y * g, y.z = y.z * f + v.z * g, y.w = y.w * f + v.w * g;
+    }
+    const int hk = rec.z / row_tiles, rr = rec.z % row_tiles * ROWS + row;
+    const int token = rec.y + rr / a.group, h = hk * a.group + rr % a.group;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    uint2 packed;
+    packed.x = pack2<E>(y.x * inv, y.y * inv), packed.y = pack2<E>(y.z * inv, y.w * inv);
+    *reinterpret_cast<uint2 *>((E *)a.out + (size_t)token * a.ldo + (size_t)h * D + 4 * c) = packed;
+    if (a.lse && c == 0)
+        a.lse[(size_t)token * a.Hkv * a.group + h] =
+            sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718056f;
+}
+
+int rows_of(int most_rows) { return most_rows <= 16 ? 16 : most_rows <= 32 ? 32 : 64; }
+
+// The workspace: the pieces' outputs, their maxima and sums, a record a CTA.
+struct Workspace {
+    size_t ml, records, bytes;
+};
+Workspace workspace(int rows, int D) {
+    const size_t ctas = (size_t)sm_count() * kCtasPerSm, pieces = 2 * ctas;
+    Workspace w;
+    w.ml = pieces * rows * D * sizeof(float);
+    w.records = w.ml + pieces * rows * 2 * sizeof(float);
+    w.bytes = w.records + ctas * sizeof(int4);
+    return w;
+}
+
+template <typename E, int D, int WR, int WK, int MT>
+cudaError_t launch_tree(const TreeArgs &a, bool pdl, cudaStream_t s) {
+    constexpr int ROWS = WR * MT * 16, smem = tree_smem_bytes<D, WR, MT>();
+    auto kernel = tree_kernel<E, D, WR, WK, MT>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const dim3 grid(sm_count() * kCtasPerSm);
+    e = launch(kernel, grid, dim3(kThreads), smem, s, pdl, a);
+    if (e != cudaSuccess) return e;
+    return launch(join_kernel<E, D, ROWS>, dim3(grid.x, ROWS * D / 4 / kThreads), dim3(kThreads), 0, s, true, a);
+}
+
+template <typename E, int D>
+cudaError_t launch_tree_rows(const TreeArgs &a, int rows, bool pdl, cudaStream_t s) {
+    if (rows == 16) return launch_tree<E, D, 1, 4, 1>(a, pdl, s);
+    if (rows == 32) return launch_tree<E, D, 1, 4, 2>(a, pdl, s);
+    return launch_tree<E, D, 2, 2, 2>(a, pdl, s);
 }
 
 }  // namespace
@@ -109,7 +598,7 @@ using namespace fb;
 extern "C" size_t fb_attn_tree_workspace_bytes(int Hq, int Hkv, int D, int max_draft) {
     if (Hq < 1 || Hq > kMaxHeads || Hkv < 1 || Hq % Hkv || (D != 64 && D != 128) || max_draft < 1 || max_draft > 64)
         return 0;
-    return 16;
+    return workspace(rows_of(max_draft * (Hq / Hkv)), D).bytes;
 }
 
 extern "C" fb_status fb_attn_tree(const void *q, int ldq, int T, int Hq, const fb_kv_cache *cache,
@@ -131,15 +620,21 @@ extern "C" fb_status fb_attn_tree(const void *q, int ldq, int T, int Hq, const f
         return FB_ERR_MISALIGNED;
     if (!ws || !aligned(ws, 16) || ws_bytes < fb_attn_tree_workspace_bytes(Hq, cache->Hkv, D, max_draft))
         return FB_ERR_WORKSPACE;
-    TreeArgs a = {q,  cache->k, cache->v,   out, lse, page_table, lens,     cu_draft,  mask,        n,
-                  T,  Hq,       cache->Hkv, ldq, ldo, table_width, ld_table, max_draft, cache->pages, log2_of(cache->page_size), scale};
-    const int64_t rows = (int64_t)T * Hq;
-    const dim3 grid((unsigned)((rows + 3) / 4)), block(kThreads);
-    const bool pdl = flags & FB_GEMV_PDL, half = cache->t == FB_F16;
+    const int group = Hq / cache->Hkv, rows = rows_of(max_draft * group);
+    const Workspace w = workspace(rows, D);
+    TreeArgs a = {};
+    a.q = q, a.kc = cache->k, a.vc = cache->v, a.out = out, a.lse = lse;
+    a.table = page_table, a.lens = lens, a.cu = cu_draft, a.mask = mask;
+    a.part = (float *)ws, a.part_ml = (float *)((char *)ws + w.ml), a.records = (int4 *)((char *)ws + w.records);
+    a.n = n, a.T = T, a.Hkv = cache->Hkv, a.group = group, a.ldq = ldq, a.ldo = ldo;
+    a.table_width = table_width, a.ld_table = ld_table, a.max_draft = max_draft;
+    a.pages = cache->pages, a.page_shift = log2_of(cache->page_size);
+    a.scale_log2 = scale * 1.44269504089f;
+    const bool pdl = flags & FB_GEMV_PDL;
     cudaStream_t s = as_stream(stream);
-    if (D == 64)
-        return status_of(half ? launch(tree_rows_kernel<__half, 64>, grid, block, 0, s, pdl, a)
-                              : launch(tree_rows_kernel<__nv_bfloat16, 64>, grid, block, 0, s, pdl, a));
-    return status_of(half ? launch(tree_rows_kernel<__half, 128>, grid, block, 0, s, pdl, a)
-                          : launch(tree_rows_kernel<__nv_bfloat16, 128>, grid, block, 0, s, pdl, a));
+    if (cache->t == FB_F16)
+        return status_of(D == 64 ? launch_tree_rows<__half, 64>(a, rows, pdl, s)
+                                 : launch_tree_rows<__half, 128>(a, rows, pdl, s));
+    return status_of(D == 64 ? launch_tree_rows<__nv_bfloat16, 64>(a, rows, pdl, s)
+                             : launch_tree_rows<__nv_bfloat16, 128>(a, rows, pdl, s));
 }

@@ -36,6 +36,7 @@
 
 #include "attn_common.cuh"
 #include "fb_internal.cuh"
+#include "tensor_core.cuh"
 
 namespace fb {
 namespace {
@@ -103,7 +104,6 @@ __device__ __forceinline__ void step(const TreeArgs &a, Cursor &c) {
     } while (c.q.row_tiles == 0);
 }
 
-__device__ __forceinline__ uint32_t smem_address(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool valid) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }

@@ -53,6 +53,10 @@ constexpr int kThreads = 384;
 constexpr int kColumns = 512;              // all of tensor memory
 constexpr int kItems = 2;                  // items known at a time
 constexpr int kItemReaders = 8 + 1 + 2;    // warps that read an item
+// Registers a thread: at the launch, then of the softmax warps and of the others; the shares of the
+// eight and the four warps add up to the launch's.
+constexpr int kLaunchRegisters = 168, kManyRegisters = 208, kFewRegisters = 88;
+static_assert(8 * kManyRegisters + 4 * kFewRegisters == 12 * kLaunchRegisters, "registers are moved, not made");
 constexpr float kRescaleLog2 = 8.0f;
 
 template <int D>
@@ -149,6 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 8) {
         // ---- items and copies -----------------------------------------------------
+        give_registers<kFewRegisters>();
         int64_t want = blockIdx.x, before = 0;   // the item wanted; the items of the sequences before the chunk
         int64_t upto = 0, chunk = 0;             // inclusive prefix within the chunk of 32 sequences, its total
         int base = -32, first = 0, len = 0;      // the chunk's first sequence; a lane's sequence of it
@@ -221,6 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 9) {
         // ---- products ---------------------------------------------------------------
+        give_registers<kFewRegisters>();
         if (lane == 0) {
             constexpr uint32_t kScores = mma_word(kBf16, kTile, kTile, false), kValues = mma_word(kBf16, kTile, D, true);
             uint32_t loads = 0, q_uses[2] = {0, 0}, p_uses[2] = {0, 0}, clean_uses = 0;   // clean_uses: a bit a place
@@ -294,6 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp >= 10) {
         // ---- values that are not finite, in the tiles on the diagonal ------------------
+        give_registers<kFewRegisters>();
         uint32_t loads = 0, asks = 0;
         bool ok = true;
         for (uint32_t count = 0; ok; ++count) {
@@ -340,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // ---- softmax and output: one row a thread ----------------------------------------
+        take_registers<kManyRegisters>();
         const int s = warp / 4, local = tid % kTile;
         const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
         const uint32_t s_at = tmem + lanes + s * kTile, o_at = tmem + lanes + 2 * kTile + s * D;
@@ -524,7 +532,11 @@ cudaError_t launch_prompt(const PromptArgs &a, const fb_heads &in, bool pdl, cud
         !head_map(&v, in.v, in.t, in.T, in.Hkv, D, in.ldv))
         return cudaErrorInvalidValue;
     auto kernel = prompt_kernel<E, D>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes<D>);
+    cudaFuncAttributes attr;
+    cudaError_t e = cudaFuncGetAttributes(&attr, kernel);
+    if (e != cudaSuccess) return e;
+    if (attr.numRegs != kLaunchRegisters) return cudaErrorInvalidValue;   // a warp would wait for registers for good
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes<D>);
     if (e != cudaSuccess) return e;
     // one CTA an SM, no more than there can be items
     const int64_t most = ((int64_t)(in.T + kBlock - 1) / kBlock + (a.n < in.T ? a.n : in.T)) * in.Hq;

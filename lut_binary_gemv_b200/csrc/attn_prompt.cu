@@ -227,77 +227,97 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 9) {
         // ---- products ---------------------------------------------------------------
         give_registers<kFewRegisters>();
-        if (lane == 0) {
-            constexpr uint32_t kScores = mma_word(kBf16, kTile, kTile, false), kValues = mma_word(kBf16, kTile, D, true);
-            uint32_t loads = 0, q_uses[2] = {0, 0}, p_uses[2] = {0, 0}, clean_uses = 0;   // clean_uses: a bit a place
-            auto scores = [&](int s, int place) {
-                const uint32_t q = tiles + s * kTileBytes<D>, k = ring + place * kTileBytes<D>;
+        // The whole warp walks through the waits, so that addresses and control are uniform; one thread issues.
+        constexpr uint32_t kScores = mma_word(kBf16, kTile, kTile, false), kValues = mma_word(kBf16, kTile, D, true);
+        const bool leader = elected();
+        struct Place {
+            uint32_t at, phase;
+            __device__ void next() {
+                if (++at == R) at = 0, phase ^= 1;
+            }
+        };
+        Place place = {0, 0};
+        uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0}, clean_phase = 0;   // clean_phase: a bit a place
+        auto scores = [&](int s, uint32_t at) {
+            const uint32_t q = tile_descriptor(tiles + s * kTileBytes<D>, 16);
+            const uint32_t k = tile_descriptor(ring + at * kTileBytes<D>, 16);
+            if (leader) {
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x) {
-                    const uint32_t at = x / 4 * (kTile * 128) + x % 4 * 32;
-                    mma_shared(tmem + s * kTile, tile_descriptor(q + at, 16), tile_descriptor(k + at, 16), kScores, x > 0);
+                    const uint32_t step = (x / 4 * (kTile * 128) + x % 4 * 32) / 16;
+                    mma_shared(tmem + s * kTile, q + step, k + step, kScores, x > 0);
                 }
                 mma_commit(bar(bars.s_full[s]));
-            };
-            auto values = [&](int s, int place, bool add) {
-                const uint32_t v = ring + place * kTileBytes<D>;
+            }
+        };
+        auto values = [&](int s, uint32_t at, bool add) {
+            const uint32_t v = tile_descriptor(ring + at * kTileBytes<D>, kTile * 128);
+            if (leader) {
 #pragma unroll
                 for (int x = 0; x < kTile / 16; ++x)
-                    mma_tensor(tmem + 2 * kTile + s * D, tmem + s * kTile + x * 8,
-                               tile_descriptor(v + x * 2048, kTile * 128), kValues, add || x > 0);
-            };
-            auto items_loop = [&]() {
-                for (uint32_t count = 0;; ++count) {
-                    const int slot = count % kItems;
-                    if (!wait(bars.item_full[slot], count / kItems & 1)) return;
-                    const int head = items[slot].head, n0 = key_tiles(items[slot], 0), n1 = key_tiles(items[slot], 1);
-                    const int n = max(n0, n1);
-                    barrier_arrive(bar(bars.item_free[slot]));
-                    if (head < 0) return;
-                    auto place = [&](int i) { return (int)((loads + i) % R); };
-                    auto arrived = [&](int i) { return wait(bars.full[place(i)], (loads + i) / R & 1); };
-                    if (!arrived(0)) return;
+                    mma_tensor(tmem + 2 * kTile + s * D, tmem + s * kTile + x * 8, v + x * (2048 / 16), kValues, add || x > 0);
+            }
+        };
+        auto commit = [&](uint64_t &b) {
+            if (leader) mma_commit(bar(b));
+        };
+        auto run = [&]() {
+            for (uint32_t count = 0;; ++count) {
+                const int slot = count % kItems;
+                if (!warp_wait(bars.item_full[slot], count / kItems & 1)) return;
+                const int head = items[slot].head;
+                const int n0 = __shfl_sync(~0u, key_tiles(items[slot], 0), 0), n1 = __shfl_sync(~0u, key_tiles(items[slot], 1), 0);
+                const int n = max(n0, n1);
+                __syncwarp();
+                if (leader) barrier_arrive(bar(bars.item_free[slot]));
+                if (head < 0) return;
+                if (!warp_wait(bars.full[place.at], place.phase)) return;
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const int ns = s ? n1 : n0;
+                    if (ns == 0) continue;
+                    if (!warp_wait(bars.q_full[s], q_phase[s])) return;
+                    q_phase[s] ^= 1;
+                    tensor_fence_after();
+                    scores(s, place.at);
+                    if (ns == 1) commit(bars.q_free[s]);
+                }
+                commit(bars.free_[place.at]);
+                place.next();
+                for (int j = 0; j < n; ++j) {
+                    const Place v = place;
+                    place.next();
+                    const Place k = place;   // the next keys
+                    if (j + 1 < n) place.next();
+                    if (!warp_wait(bars.full[v.at], v.phase)) return;
+                    if (j >= n0 - 1) {
+                        if (!warp_wait(bars.clean[v.at], clean_phase >> v.at & 1)) return;
+                        clean_phase ^= 1u << v.at;
+                    }
+                    if (j + 1 < n && !warp_wait(bars.full[k.at], k.phase)) return;
+#pragma unroll
                     for (int s = 0; s < 2; ++s) {
                         const int ns = s ? n1 : n0;
-                        if (ns == 0) continue;
-                        if (!wait(bars.q_full[s], q_uses[s]++ & 1)) return;
+                        if (j >= ns) continue;
+                        if (!warp_wait(bars.p_full[s], p_phase[s])) return;
+                        p_phase[s] ^= 1;
                         tensor_fence_after();
-                        scores(s, place(0));
-                        if (ns == 1) mma_commit(bar(bars.q_free[s]));
-                    }
-                    mma_commit(bar(bars.free_[place(0)]));
-                    for (int j = 0; j < n; ++j) {
-                        const int vp = place(2 * j + 1);
-                        if (!arrived(2 * j + 1)) return;
-                        if (j >= n0 - 1) {
-                            if (!wait(bars.clean[vp], clean_uses >> vp & 1)) return;
-                            clean_uses ^= 1u << vp;
+                        values(s, v.at, j > 0);
+                        if (j + 1 == ns) {
+                            commit(bars.o_full[s]);
+                        } else {
+                            scores(s, k.at);
+                            if (j + 2 == ns) commit(bars.q_free[s]);
                         }
-                        if (j + 1 < n && !arrived(2 * j + 2)) return;
-                        for (int s = 0; s < 2; ++s) {
-                            const int ns = s ? n1 : n0;
-                            if (j >= ns) continue;
-                            if (!wait(bars.p_full[s], p_uses[s]++ & 1)) return;
-                            tensor_fence_after();
-                            values(s, vp, j > 0);
-                            if (j + 1 == ns) {
-                                mma_commit(bar(bars.o_full[s]));
-                            } else {
-                                scores(s, place(2 * j + 2));
-                                if (j + 2 == ns) mma_commit(bar(bars.q_free[s]));
-                            }
-                        }
-                        mma_commit(bar(bars.free_[vp]));
-                        if (j + 1 < n) mma_commit(bar(bars.free_[place(2 * j + 2)]));
                     }
-                    loads += 2 * n;
+                    commit(bars.free_[v.at]);
+                    if (j + 1 < n) commit(bars.free_[k.at]);
                 }
-            };
-            items_loop();
-            mma_commit(bar(bars.done));   // no arrival of a commit is under way when the CTA's memory goes
-            wait(bars.done, 0);
-        }
-        __syncwarp();
+            }
+        };
+        run();
+        commit(bars.done);   // no arrival of a commit is under way when the CTA's memory goes
+        warp_wait(bars.done, 0);
     } else if (warp >= 10) {
         // ---- values that are not finite, in the tiles on the diagonal ------------------
         give_registers<kFewRegisters>();
@@ -367,24 +387,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 tensor_fence_after();
                 uint32_t x[4][32];
+                float top[4];
+                const bool diagonal = j == n - 1;
+                tmem_load32(x[0], s_at);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_load32(x[c], s_at + 32 * c);
-                tmem_loads_done();
-                if (j == n - 1) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < 4; ++c) {   // the maximum of one part while the next is on its way
+                    tmem_wait32(x[c]);
+                    if (c < 3) tmem_load32(x[c + 1], s_at + 32 * (c + 1));
+                    if (diagonal) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             if (32 * c + i > local) x[c][i] = 0xFF800000u;
-                }
-                float top[4];
+                    }
+                    top[c] = max3(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]), __uint_as_float(x[c][2]));
+                    float other = max3(__uint_as_float(x[c][3]), __uint_as_float(x[c][4]), __uint_as_float(x[c][5]));
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    top[c] = fmaxf(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]));
-#pragma unroll
-                    for (int i = 2; i < 32; i += 2) top[c] = max3(top[c], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
+                    for (int i = 6; i < 30; i += 4) {
+                        top[c] = max3(top[c], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
+                        other = max3(other, __uint_as_float(x[c][i + 2]), __uint_as_float(x[c][i + 3]));
+                    }
+                    top[c] = max3(top[c], __uint_as_float(x[c][30]), __uint_as_float(x[c][31]));
+                    top[c] = max3(top[c], other, other);
                 }
-                const float mn = max3(fmaxf(top[0], top[1]), top[2], top[3]) * a.scale_log2;
+                const float mn = max3(max3(top[0], top[1], top[2]), top[3], top[3]) * a.scale_log2;
                 const bool grown = mn > m + kRescaleLog2;   // also the first finite score of the row
                 if (__any_sync(~0u, grown)) {
                     const float f = grown ? exp2_approx(m - mn) : 1.0f;
@@ -393,20 +418,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (j > 0) {   // the product before is complete: this tile's scores were issued behind it
                         const uint64_t f2 = pair(f, f);
 #pragma unroll
-                        for (int c = 0; c < D; c += 32) {
-                            uint32_t o[32];
-                            tmem_load32(o, o_at + c);
-                            tmem_loads_done();
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t o[16];
+                            tmem_load16(o, o_at + c);
+                            tmem_wait16(o);
 #pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
+                            for (int i = 0; i < 16; i += 2) {
                                 float lo, hi;
                                 unpair(mul2(pair(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), f2), lo, hi);
                                 o[i] = __float_as_uint(lo), o[i + 1] = __float_as_uint(hi);
                             }
-                            tmem_store32(o_at + c, o);
+                            tmem_store16(o_at + c, o);
                         }
                     }
                 }
+                if (!(mn < INFINITY)) l = NAN;   // a score that is NaN or infinite: the row has no weights
                 const float ref = m == -INFINITY ? 0.0f : m;
                 const uint64_t ref2 = pair(-ref, -ref);
                 uint64_t sum[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
@@ -444,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
                     tmem_load32(o, o_at + c);
-                    tmem_loads_done();
+                    tmem_wait32(o);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
                     for (int t = 0; t <= s; ++t)

@@ -84,7 +84,7 @@ struct Item {
 struct Barriers {
     uint64_t q_full[2], q_free[2];          // the query tiles
     uint64_t full[8], free_[8], clean[8], ask[8];   // the ring
-    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t s_full[2], p_full[2][2], o_full[2];   // the weights by halves of the keys
     uint64_t item_full[kItems], item_free[kItems];
     uint64_t done;
 };
@@ -132,8 +132,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         gave_up_word = 0;
         for (int i = 0; i < 2; ++i) {
             barrier_init(bar(bars.q_full[i]), 1), barrier_init(bar(bars.q_free[i]), 1);
-            barrier_init(bar(bars.s_full[i]), 1), barrier_init(bar(bars.p_full[i]), 4);
-            barrier_init(bar(bars.o_full[i]), 1);
+            barrier_init(bar(bars.p_full[i][0]), 4), barrier_init(bar(bars.p_full[i][1]), 4);
+            barrier_init(bar(bars.s_full[i]), 1), barrier_init(bar(bars.o_full[i]), 1);
         }
         for (int i = 0; i < R; ++i) {
             barrier_init(bar(bars.full[i]), 1), barrier_init(bar(bars.free_[i]), 1);
@@ -154,11 +154,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 8) {
         // ---- items and copies -----------------------------------------------------
         give_registers<kFewRegisters>();
-        int64_t want = blockIdx.x, before = 0;   // the item wanted; the items of the sequences before the chunk
+        int64_t before = 0;                      // the items of the sequences before the chunk
         int64_t upto = 0, chunk = 0;             // inclusive prefix within the chunk of 32 sequences, its total
         int base = -32, first = 0, len = 0;      // the chunk's first sequence; a lane's sequence of it
         uint32_t loads = 0, q_uses[2] = {0, 0};
-        for (uint32_t count = 0;; ++count, want += gridDim.x) {
+        for (uint32_t count = 0;; ++count) {
+            // a sequence's items get shorter: every other round of CTAs runs backwards, which evens their sums out
+            const int64_t want = (int64_t)count * gridDim.x + (count & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
             while (base < a.n && want >= before + chunk) {
                 before += chunk;
                 base += 32;
@@ -250,12 +252,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mma_commit(bar(bars.s_full[s]));
             }
         };
-        auto values = [&](int s, uint32_t at, bool add) {
-            const uint32_t v = tile_descriptor(ring + at * kTileBytes<D>, kTile * 128);
+        auto values = [&](int s, uint32_t at, int h, bool add) {   // with one half of the keys
+            const uint32_t v = tile_descriptor(ring + at * kTileBytes<D> + h * (kTile / 2 * 128), kTile * 128);
             if (leader) {
 #pragma unroll
-                for (int x = 0; x < kTile / 16; ++x)
-                    mma_tensor(tmem + 2 * kTile + s * D, tmem + s * kTile + x * 8, v + x * (2048 / 16), kValues, add || x > 0);
+                for (int x = 0; x < kTile / 32; ++x)
+                    mma_tensor(tmem + 2 * kTile + s * D, tmem + s * kTile + h * 32 + x * 8, v + x * (2048 / 16), kValues,
+                               add || x > 0);
             }
         };
         auto commit = [&](uint64_t &b) {
@@ -299,10 +302,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int s = 0; s < 2; ++s) {
                         const int ns = s ? n1 : n0;
                         if (j >= ns) continue;
-                        if (!warp_wait(bars.p_full[s], p_phase[s])) return;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (!warp_wait(bars.p_full[s][h], p_phase[s])) return;
+                            tensor_fence_after();
+                            values(s, v.at, h, j > 0 || h > 0);
+                        }
                         p_phase[s] ^= 1;
-                        tensor_fence_after();
-                        values(s, v.at, j > 0);
                         if (j + 1 == ns) {
                             commit(bars.o_full[s]);
                         } else {
@@ -387,29 +393,46 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 tensor_fence_after();
                 uint32_t x[4][32];
-                float top[4];
                 const bool diagonal = j == n - 1;
-                tmem_load32(x[0], s_at);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {   // the maximum of one part while the next is on its way
-                    tmem_wait32(x[c]);
-                    if (c < 3) tmem_load32(x[c + 1], s_at + 32 * (c + 1));
-                    if (diagonal) {
+                for (int c = 0; c < 4; ++c) tmem_load32(x[c], s_at + 32 * c);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_wait32(x[c]);
+                if (diagonal) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             if (32 * c + i > local) x[c][i] = 0xFF800000u;
-                    }
-                    top[c] = max3(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]), __uint_as_float(x[c][2]));
-                    float other = max3(__uint_as_float(x[c][3]), __uint_as_float(x[c][4]), __uint_as_float(x[c][5]));
+                }
+                // The first weights are computed from the maximum so far while the new one is looked for: it
+                // seldom asks for a change, and the exponentials' unit need not wait for it.
+                uint64_t sum[2];
+                uint32_t p[16];
+                auto weights = [&](int c, float ref) {
+                    const uint64_t ref2 = pair(-ref, -ref);
 #pragma unroll
-                    for (int i = 6; i < 30; i += 4) {
-                        top[c] = max3(top[c], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
-                        other = max3(other, __uint_as_float(x[c][i + 2]), __uint_as_float(x[c][i + 3]));
+                    for (int i = 0; i < 16; ++i) {
+                        float lo, hi;
+                        unpair(fma2(pair(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])), scale2, ref2), lo, hi);
+                        lo = exp2_approx(lo), hi = exp2_approx(hi);
+                        const uint64_t both = pair(lo, hi);
+                        sum[i % 2] = c == 0 && i < 2 ? both : add2(sum[i % 2], both);
+                        p[i] = pack2<E>(lo, hi);
                     }
-                    top[c] = max3(top[c], __uint_as_float(x[c][30]), __uint_as_float(x[c][31]));
-                    top[c] = max3(top[c], other, other);
+                };
+                weights(0, m == -INFINITY ? 0.0f : m);
+                float top[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    top[c] = max3(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]), __uint_as_float(x[c][2]));
+#pragma unroll
+                    for (int i = 3; i < 31; i += 2)
+                        top[c] = max3(top[c], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
+                    top[c] = max3(top[c], __uint_as_float(x[c][31]), __uint_as_float(x[c][31]));
                 }
                 const float mn = max3(max3(top[0], top[1], top[2]), top[3], top[3]) * a.scale_log2;
+                if (!(mn < INFINITY)) l = NAN;   // a score that is NaN or infinite: the row has no weights
                 const bool grown = mn > m + kRescaleLog2;   // also the first finite score of the row
                 if (__any_sync(~0u, grown)) {
                     const float f = grown ? exp2_approx(m - mn) : 1.0f;
@@ -431,28 +454,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tmem_store16(o_at + c, o);
                         }
                     }
+                    weights(0, m == -INFINITY ? 0.0f : m);
                 }
-                if (!(mn < INFINITY)) l = NAN;   // a score that is NaN or infinite: the row has no weights
                 const float ref = m == -INFINITY ? 0.0f : m;
-                const uint64_t ref2 = pair(-ref, -ref);
-                uint64_t sum[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    uint32_t p[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float lo, hi;
-                        unpair(fma2(pair(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])), scale2, ref2), lo, hi);
-                        lo = exp2_approx(lo), hi = exp2_approx(hi);
-                        sum[i % 2] = add2(sum[i % 2], pair(lo, hi));
-                        p[i] = pack2<E>(lo, hi);
-                    }
+                    if (c > 0) weights(c, ref);
                     tmem_store16(s_at + 16 * c, p);
+                    if (c % 2) {
+                        tmem_stores_done();
+                        tensor_fence_before();
+                        __syncwarp();
+                        if (lane == 0) barrier_arrive(bar(bars.p_full[s][c / 2]));
+                    }
                 }
-                tmem_stores_done();
-                tensor_fence_before();
-                __syncwarp();
-                if (lane == 0) barrier_arrive(bar(bars.p_full[s]));
                 float lo, hi;
                 unpair(add2(sum[0], sum[1]), lo, hi);
                 l += lo + hi;

@@ -154,12 +154,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 8) {
         // ---- items and copies -----------------------------------------------------
         give_registers<kFewRegisters>();
-        int64_t before = 0;                      // the items of the sequences before the chunk
-        int64_t upto = 0, chunk = 0;             // inclusive prefix within the chunk of 32 sequences, its total
-        int base = -32, first = 0, len = 0;      // the chunk's first sequence; a lane's sequence of it
+        // Sequences are taken 32 at a time, one a lane.  Their items come longest first: by the block's
+        // place in its sequence, falling, then by sequence, then by head.  Every other round of CTAs runs
+        // backwards, which evens out what a CTA gets.
+        int64_t before = 0, chunk = 0;           // items of the chunks before, items of this one
+        int64_t level_before = 0;                // items of the chunk's levels before
+        int base = -32, first = 0, len = 0, blocks = 0, level = 0;
         uint32_t loads = 0, q_uses[2] = {0, 0};
         for (uint32_t count = 0;; ++count) {
-            // a sequence's items get shorter: every other round of CTAs runs backwards, which evens their sums out
             const int64_t want = (int64_t)count * gridDim.x + (count & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
             while (base < a.n && want >= before + chunk) {
                 before += chunk;
@@ -169,23 +171,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                     first = min(max(a.cu[base + lane], 0), a.T);
                     len = min(max(a.cu[base + lane + 1], first), a.T) - first;
                 }
-                upto = (int64_t)((len + kBlock - 1) / kBlock) * a.Hq;
-#pragma unroll
-                for (int x = 1; x < 32; x <<= 1) {
-                    const int64_t y = __shfl_up_sync(~0u, upto, x);
-                    if (lane >= x) upto += y;
-                }
-                chunk = __shfl_sync(~0u, upto, 31);
+                blocks = (len + kBlock - 1) / kBlock;
+                chunk = (int64_t)__reduce_add_sync(~0u, blocks) * a.Hq;
+                level = __reduce_max_sync(~0u, blocks) - 1;
+                level_before = 0;
             }
             Item it;
             it.head = -1, it.first = it.len = it.block = 0;
             if (base < a.n) {
-                const int src = __ffs(__ballot_sync(~0u, before + upto > want)) - 1;
+                uint32_t there = __ballot_sync(~0u, blocks > level);
+                while (want - before >= level_before + (int64_t)__popc(there) * a.Hq) {
+                    level_before += (int64_t)__popc(there) * a.Hq;
+                    there = __ballot_sync(~0u, blocks > --level);
+                }
+                const int i = (int)(want - before - level_before);
+                for (int k = i / a.Hq; k > 0; --k) there &= there - 1;
+                const int src = __ffs(there) - 1;
                 it.first = __shfl_sync(~0u, first, src), it.len = __shfl_sync(~0u, len, src);
-                const int blocks = (it.len + kBlock - 1) / kBlock;
-                const int64_t i = want - (before + __shfl_sync(~0u, upto, src) - (int64_t)blocks * a.Hq);
-                it.head = (int)(i % a.Hq);
-                it.block = blocks - 1 - (int)(i / a.Hq);   // the longest rows first
+                it.head = i % a.Hq;
+                it.block = level;
             }
             const int slot = count % kItems;
             bool ok = true;

@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 from typing import Optional, Tuple
 
 import torch
@@ -88,7 +89,7 @@ def lib() -> C.CDLL:
         L = C.CDLL(library_path)
         P, I, S = C.c_void_p, C.c_int, C.c_size_t
         W = C.POINTER(FbWeightsStruct)
-        H, KV, F, U = C.POINTER(FbHeadsStruct), C.POINTER(FbKvCacheStruct), C.c_float, C.c_uint
+        H, KV, F, U = P, P, C.c_float, C.c_uint   # the attention calls' structs, as bytes or by reference
         sig = {
             "fb_packed_words": (S, [I, I, I]),
             "fb_pack": (I, [P, I, I, I, P, P]),
@@ -430,51 +431,59 @@ def fit(W: torch.Tensor, X: torch.Tensor, K: int, Ks: int, nS: int, sweeps: int)
 
 
 # ---- attention ---------------------------------------------------------------
+#
+# Eager calls of small cases are bound by host time, so the checks below read
+# each tensor property once and the structs are packed as bytes.
+
+_HEADS = struct.Struct("@PPP8i")      # FbHeadsStruct
+_CACHE = struct.Struct("@PP5i4x")     # FbKvCacheStruct
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _on(device: torch.device, f, *args) -> int:
+def _on(device: int, f, *args) -> int:
     """f(*args, stream) on the device the tensors live on, whichever is current."""
-    if device.index is not None and device.index != torch.cuda.current_device():
+    if device != _get_device():
         with torch.cuda.device(device):
-            return f(*args, _stream(device))
-    return f(*args, _stream(device))
+            return f(*args, torch.cuda.current_stream(device).cuda_stream)
+    return f(*args, torch.cuda.current_stream(device).cuda_stream if _raw_stream is None else _raw_stream(device))
 
 
-def _head_rows(t: torch.Tensor, what: str, device=None, shape=None, dtype=None) -> int:
-    """The row pitch of [T, H, D] heads whose heads are contiguous within a row."""
-    if t.dim() != 3 or t.dtype not in _DTYPES or t.device.type != "cuda":
-        raise ValueError(f"{what}: a [T, heads, D] tensor (f32/f16/bf16) on the GPU")
-    T, H, D = t.shape
-    if shape is not None and (T, H, D) != shape:
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {shape}")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{what}: {t.dtype}, expected {dtype}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{what}: on {t.device}, expected {device}")
-    if (t.stride(2) != 1 and D > 1) or (t.stride(1) != D and H > 1):
+def _head_rows(t: torch.Tensor, what: str, device: int, shape, dtype) -> int:
+    """The row pitch of [T, H, D] heads on the GPU whose heads are contiguous within a row."""
+    st = t.stride()
+    if t.shape != shape or t.dtype != dtype or t.get_device() != device or device < 0:
+        raise ValueError(f"{what}: a {dtype} tensor {tuple(shape)} on the GPU of the others is expected, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    T, H, D = shape
+    if (st[2] != 1 and D > 1) or (st[1] != D and H > 1):
         raise ValueError(f"{what}: the heads of a row must be contiguous (only rows may be strided)")
-    return t.stride(0) if T > 1 else H * D
+    return st[0] if T > 1 else H * D
 
 
-def _flat(t: Optional[torch.Tensor], what: str, dtype, shape, device) -> Optional[int]:
-    """The address of a contiguous tensor of the given type and shape (None passes)."""
+def _sizes(q: torch.Tensor, k: torch.Tensor):
+    if q.dim() != 3 or k.dim() != 3 or q.dtype not in _DTYPES:
+        raise ValueError("q, k, v: [T, heads, D] tensors (f32/f16/bf16)")
+    return q.shape, k.shape
+
+
+def _flat(t: Optional[torch.Tensor], what: str, dtype, n: int, device: int) -> Optional[int]:
+    """The address of a contiguous tensor of n elements of the given type (None passes)."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{what}: a contiguous {dtype} tensor {tuple(shape)} on {device}")
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{what}: a contiguous {dtype} tensor of {n} elements on the GPU of the others is expected")
     return t.data_ptr()
 
 
-def _cache_struct(cache, device, dtype=None) -> FbKvCacheStruct:
-    """(k_pages, v_pages), each [pages, Hkv, page_size, D] -> the C struct."""
+def _cache_bytes(cache, device: int, dtype):
+    """(k_pages, v_pages), each [pages, Hkv, page_size, D] -> the C struct and its sizes."""
     k, v = cache
-    if (k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.dtype not in _DTYPES
-            or not k.is_contiguous() or not v.is_contiguous() or k.device != device or v.device != device
-            or (dtype is not None and k.dtype != dtype)):
+    shape = k.shape
+    if (len(shape) != 4 or v.shape != shape or k.dtype != dtype or v.dtype != dtype or not k.is_contiguous()
+            or not v.is_contiguous() or k.get_device() != device or v.get_device() != device):
         raise ValueError("cache: two contiguous [pages, Hkv, page_size, D] tensors of the heads' type and device")
-    pages, Hkv, page_size, D = k.shape
-    return FbKvCacheStruct(k=k.data_ptr(), v=v.data_ptr(), t=_DTYPES[k.dtype], pages=pages, page_size=page_size,
-                           Hkv=Hkv, D=D)
+    pages, Hkv, page_size, D = shape
+    return _CACHE.pack(k.data_ptr(), v.data_ptr(), _DTYPES[dtype], pages, page_size, Hkv, D), Hkv, D
 
 
 def rope_frequencies(rot: int, theta: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -497,36 +506,41 @@ def fb_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: Opti
     Returns (q_out, k_out, v_out): q_out is made when not given; k_out and v_out are made only where there is no
     cache.  Their type is out_dtype: by default the cache's, else a given output's, else the heads' (bf16 for
     f32 heads).  The outputs may be the inputs (in place)."""
-    dev, (T, Hq, D), Hkv = q.device, q.shape, k.shape[1] if k.dim() == 3 else 0
-    ldq = _head_rows(q, "q")
-    ldk = _head_rows(k, "k", dev, (T, Hkv, D), q.dtype)
-    ldv = _head_rows(v, "v", dev, (T, Hkv, D), q.dtype)
-    given = next((t.dtype for t in (q_out, k_out, v_out) if t is not None), None)
-    dt = out_dtype or (cache[0].dtype if cache is not None else given) or (
-        q.dtype if q.dtype != torch.float32 else torch.bfloat16)
+    qs, ks = _sizes(q, k)
+    T, Hq, D = qs
+    Hkv, dev, t = ks[1], q.get_device(), q.dtype
+    ks = (T, Hkv, D)
+    ldq, ldk, ldv = _head_rows(q, "q", dev, qs, t), _head_rows(k, "k", dev, ks, t), _head_rows(v, "v", dev, ks, t)
+    dt = out_dtype
+    if dt is None:
+        given = cache[0] if cache is not None else next((o for o in (q_out, k_out, v_out) if o is not None), None)
+        dt = given.dtype if given is not None else t if t != torch.float32 else torch.bfloat16
     if dt not in _DTYPES:
         raise ValueError("out_dtype: torch.float16 or torch.bfloat16")
-    q_out = torch.empty((T, Hq, D), dtype=dt, device=dev) if q_out is None else q_out
+    if q_out is None:
+        q_out = torch.empty(qs, dtype=dt, device=q.device)
+    kv = None
     if cache is None:
-        k_out = torch.empty((T, Hkv, D), dtype=dt, device=dev) if k_out is None else k_out
-        v_out = torch.empty((T, Hkv, D), dtype=dt, device=dev) if v_out is None else v_out
+        k_out = torch.empty(ks, dtype=dt, device=q.device) if k_out is None else k_out
+        v_out = torch.empty(ks, dtype=dt, device=q.device) if v_out is None else v_out
+    else:
+        kv = _cache_bytes(cache, dev, dt)[0]
     rot = 0 if inv_freq is None else 2 * inv_freq.numel()
     if rot and pos is None:
         raise ValueError("pos: int32 [T] where there is a rotation")
     if (cache is None) != (slots is None):
         raise ValueError("cache and slots go together")
-    hin = FbHeadsStruct(q.data_ptr(), k.data_ptr(), v.data_ptr(), _DTYPES[q.dtype], T, Hq, Hkv, D, ldq, ldk, ldv)
-    hout = FbHeadsStruct(q_out.data_ptr(), _ptr(k_out), _ptr(v_out), _DTYPES[dt], T, Hq, Hkv, D,
-                         _head_rows(q_out, "q_out", dev, (T, Hq, D), dt),
-                         0 if k_out is None else _head_rows(k_out, "k_out", dev, (T, Hkv, D), dt),
-                         0 if v_out is None else _head_rows(v_out, "v_out", dev, (T, Hkv, D), dt))
-    kv = None if cache is None else C.byref(_cache_struct(cache, dev, dt))
-    _check(_on(dev, lib().fb_qk_norm_rope, C.byref(hin), C.byref(hout), _flat(pos, "pos", torch.int32, (T,), dev),
-               _flat(inv_freq, "inv_freq", torch.float64, (rot // 2,), dev), rot,
-               _flat(q_weight, "q_weight", torch.float32, (D,), dev),
-               _flat(k_weight, "k_weight", torch.float32, (D,), dev), eps, kv,
-               _flat(slots, "slots", torch.int32, (T,), dev), flags | (FB_ROPE_NEIGHBOURS if interleaved else 0)),
-           "fb_qk_norm_rope")
+    hin = _HEADS.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), _DTYPES[t], T, Hq, Hkv, D, ldq, ldk, ldv)
+    hout = _HEADS.pack(q_out.data_ptr(), 0 if k_out is None else k_out.data_ptr(),
+                       0 if v_out is None else v_out.data_ptr(), _DTYPES[dt], T, Hq, Hkv, D,
+                       _head_rows(q_out, "q_out", dev, qs, dt),
+                       0 if k_out is None else _head_rows(k_out, "k_out", dev, ks, dt),
+                       0 if v_out is None else _head_rows(v_out, "v_out", dev, ks, dt))
+    _check(_on(dev, lib().fb_qk_norm_rope, hin, hout, _flat(pos, "pos", torch.int32, T, dev),
+               _flat(inv_freq, "inv_freq", torch.float64, rot // 2, dev), rot,
+               _flat(q_weight, "q_weight", torch.float32, D, dev), _flat(k_weight, "k_weight", torch.float32, D, dev),
+               eps, kv, _flat(slots, "slots", torch.int32, T, dev),
+               flags | FB_ROPE_NEIGHBOURS if interleaved else flags), "fb_qk_norm_rope")
     return q_out, k_out, v_out
 
 
@@ -537,16 +551,18 @@ def fb_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens
     strided), sequence s being tokens cu_seqlens[s] .. cu_seqlens[s+1]-1 (int32 [n+1]) -> [T, Hq, D].  scale
     defaults to D^-0.5; lse float32 [T, Hq] takes the logarithms of the softmax's sums.  Rows of no sequence keep
     what `out` holds (unset memory when it is not given)."""
-    dev, (T, Hq, D), Hkv = q.device, q.shape, k.shape[1] if k.dim() == 3 else 0
-    h = FbHeadsStruct(q.data_ptr(), k.data_ptr(), v.data_ptr(), _DTYPES.get(q.dtype, -1), T, Hq, Hkv, D,
-                      _head_rows(q, "q"), _head_rows(k, "k", dev, (T, Hkv, D), q.dtype),
-                      _head_rows(v, "v", dev, (T, Hkv, D), q.dtype))
-    out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev) if out is None else out
+    qs, ks = _sizes(q, k)
+    T, Hq, D = qs
+    Hkv, dev, t = ks[1], q.get_device(), q.dtype
+    ks = (T, Hkv, D)
+    h = _HEADS.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), _DTYPES[t], T, Hq, Hkv, D,
+                    _head_rows(q, "q", dev, qs, t), _head_rows(k, "k", dev, ks, t), _head_rows(v, "v", dev, ks, t))
+    if out is None:
+        out = torch.empty(qs, dtype=t, device=q.device)
     n = cu_seqlens.numel() - 1
-    _check(_on(dev, lib().fb_attn_prompt, C.byref(h), _flat(cu_seqlens, "cu_seqlens", torch.int32, (n + 1,), dev), n,
-               D ** -0.5 if scale is None else scale, out.data_ptr(),
-               _head_rows(out, "out", dev, (T, Hq, D), q.dtype), _flat(lse, "lse", torch.float32, (T, Hq), dev),
-               flags), "fb_attn_prompt")
+    _check(_on(dev, lib().fb_attn_prompt, h, _flat(cu_seqlens, "cu_seqlens", torch.int32, n + 1, dev), n,
+               D ** -0.5 if scale is None else scale, out.data_ptr(), _head_rows(out, "out", dev, qs, t),
+               _flat(lse, "lse", torch.float32, T * Hq, dev), flags), "fb_attn_prompt")
     return out
 
 
@@ -565,25 +581,30 @@ def fb_attn_tree(q: torch.Tensor, cache, page_table: torch.Tensor, lens: torch.T
     cache at positions lens[s] + j.  mask int64 [T]: bit j of a token's word lets it see drafted token j of its
     sequence (None: a chain, j <= i).  Returns [T, Hq, D]; scale, out and lse as for fb_attn_prompt.  ws (uint8)
     is made when not given."""
-    dev, (T, Hq, D) = q.device, q.shape
-    ldq = _head_rows(q, "q")
-    kv = _cache_struct(cache, dev, q.dtype)
-    if kv.D != D:
+    if q.dim() != 3:
+        raise ValueError("q: a [T, heads, D] tensor of the cache's type")
+    qs, t, dev = q.shape, q.dtype, q.get_device()
+    T, Hq, D = qs
+    ldq = _head_rows(q, "q", dev, qs, t)
+    kv, Hkv, width = _cache_bytes(cache, dev, t)
+    if width != D:
         raise ValueError("cache: another head width than q's")
     n = lens.numel()
-    if page_table.dim() != 2 or page_table.shape[0] != n or page_table.stride(1) != 1 or (
-            page_table.dtype != torch.int32) or page_table.device != dev:
+    ts = page_table.shape
+    if len(ts) != 2 or ts[0] != n or page_table.dtype != torch.int32 or page_table.get_device() != dev or (
+            page_table.stride(1) != 1 and ts[1] > 1):
         raise ValueError("page_table: an int32 [n, width] tensor with unit column stride on q's device")
-    ld_table = page_table.stride(0) if n > 1 else page_table.shape[1]
-    out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev) if out is None else out
+    if out is None:
+        out = torch.empty(qs, dtype=t, device=q.device)
     if ws is None:
-        ws = torch.empty(max(fb_attn_tree_workspace_bytes(Hq, kv.Hkv, D, max_draft), 16), dtype=torch.uint8,
-                         device=dev)
-    _check(_on(dev, lib().fb_attn_tree, q.data_ptr(), ldq, T, Hq, C.byref(kv), page_table.data_ptr(),
-               page_table.shape[1], ld_table,
-               _flat(lens, "lens", torch.int32, (n,), dev), _flat(cu_draft, "cu_draft", torch.int32, (n + 1,), dev),
-               n, max_draft, _flat(mask, "mask", torch.int64, (T,), dev), D ** -0.5 if scale is None else scale,
-               out.data_ptr(), _head_rows(out, "out", dev, (T, Hq, D), q.dtype),
-               _flat(lse, "lse", torch.float32, (T, Hq), dev), ws.data_ptr(), ws.numel() * ws.element_size(), flags),
-           "fb_attn_tree")
+        ws = torch.empty(max(lib().fb_attn_tree_workspace_bytes(Hq, Hkv, D, max_draft), 16), dtype=torch.uint8,
+                         device=q.device)
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws: a contiguous tensor on q's device")
+    _check(_on(dev, lib().fb_attn_tree, q.data_ptr(), ldq, T, Hq, kv, page_table.data_ptr(), ts[1],
+               page_table.stride(0) if n > 1 else ts[1], _flat(lens, "lens", torch.int32, n, dev),
+               _flat(cu_draft, "cu_draft", torch.int32, n + 1, dev), n, max_draft,
+               _flat(mask, "mask", torch.int64, T, dev), D ** -0.5 if scale is None else scale, out.data_ptr(),
+               _head_rows(out, "out", dev, qs, t), _flat(lse, "lse", torch.float32, T * Hq, dev), ws.data_ptr(),
+               ws.numel() * ws.element_size(), flags), "fb_attn_tree")
     return out

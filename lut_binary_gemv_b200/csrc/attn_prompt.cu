@@ -37,7 +37,6 @@
 #include <math.h>
 #include <stdint.h>
 
-#include <atomic>
 #include <type_traits>
 
 #include "attn_common.cuh"
@@ -538,26 +537,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---- host ---------------------------------------------------------------------------
 
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_tiled() {
-    static std::atomic<EncodeTiled> cached{nullptr};
-    EncodeTiled f = cached.load(std::memory_order_relaxed);
-    if (!f) {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult found;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) !=
-                cudaSuccess ||
-            found != cudaDriverEntryPointSuccess)
-            return nullptr;
-        f = reinterpret_cast<EncodeTiled>(p);
-        cached.store(f, std::memory_order_relaxed);
-    }
-    return f;
-}
-
 // [token][head][D] in boxes of 64 columns, one head and a tile of tokens.
 bool head_map(CUtensorMap *map, void *base, fb_dtype t, int T, int H, int D, int ld) {
     const EncodeTiled f = encode_tiled();
@@ -570,6 +549,18 @@ bool head_map(CUtensorMap *map, void *base, fb_dtype t, int T, int H, int D, int
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Whether the compiler gave the kernel the registers that its warps' shares add up to.
+template <auto Kernel>
+bool registers_as_planned() {
+    static std::atomic<int> registers{0};
+    if (!registers.load(std::memory_order_relaxed)) {
+        cudaFuncAttributes attr;
+        if (cudaFuncGetAttributes(&attr, Kernel) != cudaSuccess) return false;
+        registers.store(attr.numRegs, std::memory_order_relaxed);
+    }
+    return registers.load(std::memory_order_relaxed) == kLaunchRegisters;
+}
+
 template <typename E, int D>
 cudaError_t launch_prompt(const PromptArgs &a, const fb_heads &in, bool pdl, cudaStream_t s) {
     CUtensorMap q, k, v;
@@ -577,11 +568,8 @@ cudaError_t launch_prompt(const PromptArgs &a, const fb_heads &in, bool pdl, cud
         !head_map(&v, in.v, in.t, in.T, in.Hkv, D, in.ldv))
         return cudaErrorInvalidValue;
     auto kernel = prompt_kernel<E, D>;
-    cudaFuncAttributes attr;
-    cudaError_t e = cudaFuncGetAttributes(&attr, kernel);
-    if (e != cudaSuccess) return e;
-    if (attr.numRegs != kLaunchRegisters) return cudaErrorInvalidValue;   // a warp would wait for registers for good
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes<D>);
+    if (!registers_as_planned<prompt_kernel<E, D>>()) return cudaErrorInvalidValue;   // a warp would wait for registers for good
+    cudaError_t e = allow_shared<prompt_kernel<E, D>>(kSmemBytes<D>);
     if (e != cudaSuccess) return e;
     // one CTA an SM, no more than there can be items
     const int64_t most = ((int64_t)(in.T + kBlock - 1) / kBlock + (a.n < in.T ? a.n : in.T)) * in.Hq;

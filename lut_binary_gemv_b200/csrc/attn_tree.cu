@@ -16,10 +16,11 @@
 //    in the workspace (a CTA has at most two such pieces, its first and its
 //    last), and join_kernel joins them in order, so results do not depend on
 //    timing.
-//  * Of a tile, each warp owns 16 keys for all rows (up to 32 of them): it
-//    loads them itself with asynchronous copies two tiles ahead, across the
-//    ends of sequences, and needs no CTA barrier until the piece ends.  From 33
-//    rows on two warps share 32 keys and split 64 rows.
+//  * Of a tile, each warp owns 16 keys for all rows (up to 32 of them): one
+//    thread asks for them with tiled copies two tiles ahead, across the ends of
+//    sequences, and the warp needs no CTA barrier until the piece ends.  (Pages
+//    of fewer than 16 rows are copied row by row.)  From 33 rows on two warps
+//    share 32 keys and split 64 rows.
 //  * Scores and outputs are m16n8k16 products with fp32 accumulators; the
 //    weights stay in registers between the two.
 //
@@ -32,6 +33,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "attn_common.cuh"
@@ -46,6 +48,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kTileKeys = 64;      // keys of a tile, 16 loaded by each warp
 constexpr int kCtasPerSm = 2;
 constexpr int kMinTiles = 2;       // key tiles of a run, at least
+constexpr float kRescaleLog2 = 8.0f;
 
 __device__ unsigned int g_attn_errors;
 
@@ -57,6 +60,7 @@ struct TreeArgs {
     const uint64_t *mask;
     float *part, *part_ml;
     int4 *records;
+    unsigned int *errors;
     int n, T, Hkv, group, ldq, ldo, table_width, ld_table, max_draft, pages, page_shift;
     float scale_log2;
 };
@@ -138,12 +142,11 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Byte offset of the 16-byte chunk of a row in a tile of 16-bit rows: the
-// chunk index is turned by the row, so that the eight rows of a matrix load
-// lie in eight different groups of banks.
-template <int D>
+// Byte offset of a 16-byte chunk in a block of 16 rows: columns in groups of 64
+// (128 bytes a row), the chunk's index turned by the row, as the tiled copies
+// put it; the eight rows of a matrix load lie in eight different groups of banks.
 __device__ __forceinline__ int chunk_at(int row, int chunk) {
-    return row * (D * 2) + ((chunk ^ (row & 7)) << 4);
+    return (chunk >> 3) * 2048 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
 }
 
 template <typename E>
@@ -160,33 +163,47 @@ __device__ __forceinline__ uint32_t finite_part(uint32_t pair) {
 }
 
 template <int D>
-constexpr int kStages = 384 / D;   // 96 KB of tiles in flight a CTA, two CTAs an SM
+constexpr int kStages = 384 / D;   // 96 KB of tiles a CTA, two CTAs an SM
 template <int D>
-constexpr int kStageBytes = kTileKeys * D * 2 * 2;
+constexpr int kSlice = 16 * D * 4;  // a warp's share of a tile's place: 16 keys, then their values
+template <int D>
+constexpr int kStageBytes = kWarps * kSlice<D>;
 
-template <int D, int WR, int MT>
+template <int D, int ROWS>
 constexpr int tree_smem_bytes() {
-    return kStages<D> * kStageBytes<D> + WR * MT * 16 * D * 2;
+    return kStages<D> * kStageBytes<D> + ROWS * D * 2;
 }
 
-// WR row warps times WK key warps; MT row tiles of 16 a warp.
-template <typename E, int D, int WR, int WK, int MT>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const TreeArgs a) {
+// WR row warps times WK key warps; MT row tiles of 16 a warp; kTiled: pages of at least 16 rows.
+template <typename E, int D, int WR, int WK, int MT, bool kTiled>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    tree_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     static_assert(WR * WK == kWarps, "four warps");
     constexpr int ROWS = WR * MT * 16;
     constexpr int KW = kTileKeys / WK;      // keys a warp multiplies
     constexpr int NT = KW / 8;              // 8-key columns of its scores
     constexpr int CH = D / 8;               // 16-byte chunks of a row
     constexpr int S = kStages<D>;
-    constexpr int kHalfStage = kTileKeys * D * 2;
+    constexpr int kHalf = kSlice<D> / 2;    // from a slice's keys to its values
+    constexpr bool kOwnKeys = WK == kWarps; // a warp multiplies the keys it loads, and no others
+    constexpr bool kQueriesHeld = MT == 1;  // the queries stay in registers
     extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ __align__(8) uint64_t full[S][kWarps];
     __shared__ uint64_t s_mask[ROWS];
     __shared__ float s_ml[2][kWarps][MT * 16];
+    __shared__ int gave_up_word;
+    volatile int *gave_up = &gave_up_word;
 
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int wr = warp % WR, wk = warp / WR;
     const uint32_t stages = smem_address(smem), q_at = stages + S * kStageBytes<D>;
 
+    if (tid == 0) {
+        gave_up_word = 0;
+        for (int i = 0; i < S * kWarps; ++i) barrier_init(smem_address(&full[i / kWarps][i % kWarps]), 1);
+        barrier_inits_done();
+    }
+    __syncthreads();
     wait_for_previous_kernel();
 
     // ---- this CTA's run of key tiles -----------------------------------------
@@ -194,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const TreeAr
     for (int s = lane; s < a.n; s += 32) {
         const Seq q = sequence<ROWS>(a, s);
         total += (int64_t)q.row_tiles * a.Hkv * q.tiles;
-        if (q.too_many && blockIdx.x == 0 && warp == 0) atomicOr(&g_attn_errors, 2u);
+        if (q.too_many && blockIdx.x == 0 && warp == 0) atomicOr(a.errors, 2u);
     }
 #pragma unroll
     for (int x = 16; x; x >>= 1) total += __shfl_xor_sync(~0u, total, x);
@@ -239,42 +256,75 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const TreeAr
     Cursor ahead = at;
     int64_t to_load = left;
     int load_stage = 0;
+    // the page of a key position of the cursor's sequence (-1 beyond the table)
+    auto page_of = [&](int p) {
+        const int slot = p >> a.page_shift;
+        return p < ahead.q.len + ahead.q.m && slot < a.table_width ? a.table[(size_t)ahead.s * a.ld_table + slot] : -1;
+    };
+    int page = page_of(ahead.kt * kTileKeys + 16 * warp + (kTiled ? 0 : lane % 16));   // looked up a tile early
     auto load_tile = [&]() {
         if (to_load > 0) {
-            const int hk = ahead.item / ahead.q.row_tiles;
-            // lane r (and r + 16) finds the row of key r: its element offset, -1 behind the keys, -2 on a bad page
-            int64_t off = -1;
-            const int p = ahead.kt * kTileKeys + 16 * warp + lane % 16;
-            if (p < ahead.q.len + ahead.q.m) {
-                const int slot = p >> a.page_shift;
-                const int page = slot < a.table_width ? a.table[(size_t)ahead.s * a.ld_table + slot] : -1;
-                if (page >= 0 && page < a.pages) {
-                    off = ((((int64_t)page * a.Hkv + hk) << a.page_shift) + (p - (slot << a.page_shift))) * D;
-                } else {
-                    off = -2;
-                    atomicOr(&g_attn_errors, 2u);
+            const int hk = ahead.item / ahead.q.row_tiles, keys = ahead.q.len + ahead.q.m;
+            const uint32_t k_at = stages + load_stage * kStageBytes<D> + warp * kSlice<D>, v_at = k_at + kHalf;
+            const int p0 = ahead.kt * kTileKeys + 16 * warp;
+            if constexpr (kTiled) {
+                const uint32_t bar = smem_address(&full[load_stage][warp]);
+                const bool good = page >= 0 && page < a.pages;
+                if (p0 < keys && !good) {   // no such page: the rows that see it become NaN
+                    for (int i = lane; i < kSlice<D> / 16; i += 32)
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(k_at + 16 * i), "r"(0x7FFF7FFFu) : "memory");
+                    writes_before_async();
+                    __syncwarp();
                 }
-            }
-            const uint32_t k_at = stages + load_stage * kStageBytes<D>, v_at = k_at + kHalfStage;
-            const int chunk = lane % CH;
+                if (lane == 0) {
+                    if (p0 < keys && good) {
+                        const int row = p0 & ((1 << a.page_shift) - 1);
+                        barrier_expect(bar, kSlice<D>);
 #pragma unroll
-            for (int i = 0; i < 16 * CH / 32; ++i) {
-                const int r = i * (32 / CH) + lane / CH;
-                const int64_t o = __shfl_sync(~0u, off, r);
-                const int d = chunk_at<D>(16 * warp + r, chunk);
-                if (o == -2) {
-                    asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(k_at + d), "r"(0x7FFF7FFFu) : "memory");
-                    asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(v_at + d), "r"(0x7FFF7FFFu) : "memory");
-                } else {
-                    const int64_t e = o < 0 ? 0 : o + chunk * 8;
-                    copy16(k_at + d, (const E *)a.kc + e, o >= 0);
-                    copy16(v_at + d, (const E *)a.vc + e, o >= 0);
+                        for (int c = 0; c < D / 64; ++c) {
+                            tile_copy4(k_at + c * 2048, &k_map, 64 * c, row, hk, page, bar);
+                            tile_copy4(v_at + c * 2048, &v_map, 64 * c, row, hk, page, bar);
+                        }
+                    } else {
+                        if (p0 < keys) atomicOr(a.errors, 2u);
+                        barrier_arrive(bar);
+                    }
+                }
+                __syncwarp();
+            } else {
+                // lane r (and r + 16) has the row of key r: its element offset, -1 behind the keys, -2 on a bad page
+                int64_t off = -1;
+                const int p = p0 + lane % 16;
+                if (p < keys) {
+                    if (page >= 0 && page < a.pages) {
+                        off = ((((int64_t)page * a.Hkv + hk) << a.page_shift) + (p & ((1 << a.page_shift) - 1))) * D;
+                    } else {
+                        off = -2;
+                        atomicOr(a.errors, 2u);
+                    }
+                }
+                const int chunk = lane % CH;
+#pragma unroll
+                for (int i = 0; i < 16 * CH / 32; ++i) {
+                    const int r = i * (32 / CH) + lane / CH;
+                    const int64_t o = __shfl_sync(~0u, off, r);
+                    const int d = chunk_at(r, chunk);
+                    if (o == -2) {
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(k_at + d), "r"(0x7FFF7FFFu) : "memory");
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(v_at + d), "r"(0x7FFF7FFFu) : "memory");
+                    } else {
+                        const int64_t e = o < 0 ? 0 : o + chunk * 8;
+                        copy16(k_at + d, (const E *)a.kc + e, o >= 0);
+                        copy16(v_at + d, (const E *)a.vc + e, o >= 0);
+                    }
                 }
             }
-            --to_load;
-            if (to_load > 0) step<ROWS>(a, ahead);
+            if (--to_load > 0) {
+                step<ROWS>(a, ahead);
+                page = page_of(ahead.kt * kTileKeys + 16 * warp + (kTiled ? 0 : lane % 16));
+            }
         }
-        copies_close();
+        if (!kTiled) copies_close();
         load_stage = load_stage + 1 == S ? 0 : load_stage + 1;
     };
 #pragma unroll
@@ -282,6 +332,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const TreeAr
 
     // ---- the pieces -------------------------------------------------------------
     int stage = 0, last_stage = 0;
+    uint32_t phase = 0;
     while (left > 0) {
         const Seq q = at.q;
         const int hk = at.item / q.row_tiles, rt = at.item % q.row_tiles;
@@ -297,8 +348,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const TreeAr
                 const int token = q.first + rr / a.group, h = hk * a.group + rr % a.group;
                 v = *reinterpret_cast<const uint4 *>((const E *)a.q + (size_t)token * a.ldq + (size_t)h * D + c * 8);
             }
-            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(q_at + chunk_at<D>(r, c)), "r"(v.x), "r"(v.y),
-                         "r"(v.z), "r"(v.w)
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(q_at + r / 16 * kHalf + chunk_at(r % 16, c)), "r"(v.x),
+                         "r"(v.y), "r"(v.z), "r"(v.w)
                          : "memory");
         }
         if (tid < ROWS) {
@@ -308,37 +359,58 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const TreeAr
             s_mask[tid] = q.m < 64 ? bits & ((1ull << q.m) - 1) : bits;
         }
         __syncthreads();
+        auto queries = [&](int t, int d, uint32_t (&r)[4]) {
+            ldmatrix4(r, q_at + (wr * MT + t) * kHalf + chunk_at(lane % 16, 2 * d + lane / 16));
+        };
+        uint32_t held[kQueriesHeld ? D / 16 : 1][4];
+        if constexpr (kQueriesHeld) {
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) queries(0, d, held[d]);
+        }
 
         float o[MT][D / 8][4] = {};
-        float m[MT][2], l[MT][2];
+        float m[MT][2], l[MT][2];   // m: the (scaled) maximum that the weights so far are relative to
 #pragma unroll
         for (int t = 0; t < MT; ++t) m[t][0] = m[t][1] = -INFINITY, l[t][0] = l[t][1] = 0.0f;
 
         for (int kt = kt0; kt < kt1; ++kt) {
-            copies_wait<S - 2>();
-            if (WK == kWarps) __syncwarp();
+            if constexpr (kTiled) {
+                if (kOwnKeys) {
+                    barrier_wait(smem_address(&full[stage][warp]), phase, gave_up);
+                } else {
+                    for (int i = 0; i < KW / 16; ++i) barrier_wait(smem_address(&full[stage][wk * (KW / 16) + i]), phase, gave_up);
+                }
+            } else {
+                copies_wait<S - 2>();
+            }
+            if (kOwnKeys) __syncwarp();
             else __syncthreads();
             load_tile();   // into the place of the tile before, which its readers have left
-            const uint32_t k_at = stages + stage * kStageBytes<D>, v_at = k_at + kHalfStage;
-            const int key0 = wk * KW;
+            const uint32_t keys_at = stages + stage * kStageBytes<D> + wk * (KW / 16) * kSlice<D>, values_at = keys_at + kHalf;
 
             float s[MT][NT][4] = {};
 #pragma unroll
             for (int d = 0; d < D / 16; ++d) {
                 uint32_t qa[MT][4];
 #pragma unroll
-                for (int t = 0; t < MT; ++t)
-                    ldmatrix4(qa[t], q_at + chunk_at<D>((wr * MT + t) * 16 + lane % 16, 2 * d + lane / 16));
+                for (int t = 0; t < MT; ++t) {
+                    if constexpr (kQueriesHeld) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) qa[t][x] = held[d][x];
+                    } else {
+                        queries(t, d, qa[t]);
+                    }
+                }
 #pragma unroll
                 for (int j = 0; j < NT; j += 2) {
                     uint32_t kb[4];
-                    ldmatrix4(kb, k_at + chunk_at<D>(key0 + 8 * j + lane % 8 + (lane / 16) * 8, 2 * d + (lane / 8) % 2));
+                    ldmatrix4(kb, keys_at + j / 2 * kSlice<D> + chunk_at(lane % 8 + (lane / 16) * 8, 2 * d + (lane / 8) % 2));
 #pragma unroll
                     for (int t = 0; t < MT; ++t) mma<E>(s[t][j], qa[t], kb[0], kb[1]), mma<E>(s[t][j + 1], qa[t], kb[2], kb[3]);
                 }
             }
 
-            const int tile_key = kt * kTileKeys;
+            const int tile_key = kt * kTileKeys, key0 = wk * KW;
             const bool partly = tile_key + kTileKeys > q.len;   // some keys are drafted, or behind the last
             if (partly) {
 #pragma unroll
@@ -357,20 +429,41 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const TreeAr
                     }
             }
 
+            // The outputs are rescaled only when a row's maximum has grown by more than 2^8 since the last time:
+            // the sum carries the same factor, and weights up to 2^8 lose nothing in either type.
+            float top[MT][2];
+            bool grown = false;
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    float x = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) x = fmaxf(x, fmaxf(s[t][j][2 * half], s[t][j][2 * half + 1]));
+                    x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
+                    x = fmaxf(x, __shfl_xor_sync(~0u, x, 2));
+                    top[t][half] = x * a.scale_log2;
+                    grown |= top[t][half] > m[t][half] + kRescaleLog2;   // also the first finite score of a row
+                }
+            if (__any_sync(~0u, grown)) {
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const bool up = top[t][half] > m[t][half] + kRescaleLog2;
+                        const float f = up ? exp2_approx(m[t][half] - top[t][half]) : 1.0f;
+                        if (up) m[t][half] = top[t][half];
+                        l[t][half] *= f;
+#pragma unroll
+                        for (int j = 0; j < D / 8; ++j) o[t][j][2 * half] *= f, o[t][j][2 * half + 1] *= f;
+                    }
+            }
             uint32_t pa[MT][NT / 2][4];
 #pragma unroll
             for (int t = 0; t < MT; ++t)
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) top = fmaxf(top, fmaxf(s[t][j][2 * half], s[t][j][2 * half + 1]));
-                    top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-                    const float mn = fmaxf(m[t][half], top * a.scale_log2);
-                    const float ref = mn == -INFINITY ? 0.0f : mn;
-                    const float f = exp2_approx(m[t][half] - ref);
-                    m[t][half] = mn;
+                    const float ref = m[t][half] == -INFINITY ? 0.0f : m[t][half];
                     float sum = 0.0f;
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
@@ -379,21 +472,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const TreeAr
                         sum += p0 + p1;
                         pa[t][j / 2][(j % 2) * 2 + half] = pack2<E>(p0, p1);
                     }
-                    l[t][half] = l[t][half] * f + sum;
-#pragma unroll
-                    for (int j = 0; j < D / 8; ++j) o[t][j][2 * half] *= f, o[t][j][2 * half + 1] *= f;
+                    l[t][half] += sum;
                 }
 
             if (partly) {
                 // values that are not finite: scanned by the warp that loaded them
+                const uint32_t own = stages + stage * kStageBytes<D> + warp * kSlice<D> + kHalf;
                 bool odd = false;
-                for (int i = lane; i < 16 * CH; i += 32) {
-                    const uint32_t x = v_at + chunk_at<D>(16 * warp + i / CH, i % CH);
+                for (int i = lane; i < kHalf / 16; i += 32) {
                     uint4 v;
-                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(x) : "memory");
+                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(own + 16 * i) : "memory");
                     odd |= not_finite<E>(v.x) || not_finite<E>(v.y) || not_finite<E>(v.z) || not_finite<E>(v.w);
                 }
-                odd = WK == kWarps ? __any_sync(~0u, odd) : __syncthreads_or(odd);
+                odd = kOwnKeys ? __any_sync(~0u, odd) : __syncthreads_or(odd);
                 if (odd) {
                     for (int kk = 0; kk < KW; ++kk) {
                         const int dj = tile_key + key0 + kk - q.len;
@@ -406,7 +497,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const TreeAr
 #pragma unroll
                                 for (int j = 0; j < D / 8; ++j) {
                                     uint32_t v;
-                                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(v_at + chunk_at<D>(key0 + kk, j) + 4 * (lane % 4)) : "memory");
+                                    asm volatile("ld.shared.b32 %0, [%1];"
+                                                 : "=r"(v)
+                                                 : "r"(values_at + kk / 16 * kSlice<D> + chunk_at(kk % 16, j) + 4 * (lane % 4))
+                                                 : "memory");
                                     if (not_finite<E>(v)) {
                                         const float2 f = unpack2<E>(v ^ finite_part<E>(v));
                                         o[t][j][2 * half] += f.x, o[t][j][2 * half + 1] += f.y;
@@ -414,15 +508,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const TreeAr
                                 }
                             }
                     }
-                    if (WK == kWarps) __syncwarp();
+                    if (kOwnKeys) __syncwarp();
                     else __syncthreads();
-                    for (int i = lane; i < 16 * CH * 4; i += 32) {
-                        const uint32_t x = v_at + chunk_at<D>(16 * warp + i / (4 * CH), i / 4 % CH) + 4 * (i % 4);
+                    for (int i = lane; i < kHalf / 4; i += 32) {
                         uint32_t v;
-                        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(x) : "memory");
-                        if (not_finite<E>(v)) asm volatile("st.shared.b32 [%0], %1;" ::"r"(x), "r"(finite_part<E>(v)) : "memory");
+                        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(own + 4 * i) : "memory");
+                        if (not_finite<E>(v)) asm volatile("st.shared.b32 [%0], %1;" ::"r"(own + 4 * i), "r"(finite_part<E>(v)) : "memory");
                     }
-                    if (WK == kWarps) __syncwarp();
+                    writes_before_async();
+                    if (kOwnKeys) __syncwarp();
                     else __syncthreads();
                 }
             }
@@ -432,14 +526,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const TreeAr
 #pragma unroll
                 for (int d = 0; d < D / 16; ++d) {
                     uint32_t vb[4];
-                    ldmatrix4_trans(vb, v_at + chunk_at<D>(key0 + 16 * c + lane % 16, 2 * d + lane / 16));
+                    ldmatrix4_trans(vb, values_at + c * kSlice<D> + chunk_at(lane % 16, 2 * d + lane / 16));
 #pragma unroll
                     for (int t = 0; t < MT; ++t)
                         mma<E>(o[t][2 * d], pa[t][c], vb[0], vb[1]), mma<E>(o[t][2 * d + 1], pa[t][c], vb[2], vb[3]);
                 }
 
             last_stage = stage;
-            stage = stage + 1 == S ? 0 : stage + 1;
+            if (++stage == S) stage = 0, phase ^= 1;
             step<ROWS>(a, at);
         }
 
@@ -458,8 +552,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const TreeAr
             }
         const bool whole = kt0 == 0 && kt1 == q.tiles;
         const size_t piece = 2 * (size_t)blockIdx.x + (kt0 == 0 ? 1 : 0);
-        constexpr int kSlice = 16 * D * 4;
-        static_assert(kSlice * kWarps == kStageBytes<D>, "a warp's 16 rows in fp32 fill its share of a tile's place");
         uint8_t *join = smem + last_stage * kStageBytes<D>;
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
@@ -469,26 +561,27 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const TreeAr
 #pragma unroll
                 for (int j = 0; j < D / 8; ++j) {
                     const int r = half * 8 + lane / 4, c = 2 * j + (lane % 4) / 2;
-                    *reinterpret_cast<float2 *>(join + warp * kSlice + r * D * 4 + ((c ^ (r & 7) * 2) << 4) + (lane % 2) * 8) =
+                    *reinterpret_cast<float2 *>(join + warp * kSlice<D> + r * D * 4 + ((c ^ (r & 7) * 2) << 4) + (lane % 2) * 8) =
                         make_float2(o[t][j][2 * half], o[t][j][2 * half + 1]);
                 }
+            writes_before_async();
             __syncthreads();
             // warp (wr, wk) takes the columns wk of WK of its row warp's 16 rows, four at a time
             constexpr int CW = D / 4 / WK;                     // chunks of four columns a warp joins
             for (int i = lane; i < 16 * CW; i += 32) {
                 const int r = i / CW, c = wk * CW + i % CW, row = (wr * MT + t) * 16 + r;
                 if (row >= rows) continue;
-                float top = -INFINITY;
+                float best = -INFINITY;
 #pragma unroll
-                for (int x = 0; x < WK; ++x) top = fmaxf(top, s_ml[0][x * WR + wr][t * 16 + r]);
-                const float ref = top == -INFINITY ? 0.0f : top;
+                for (int x = 0; x < WK; ++x) best = fmaxf(best, s_ml[0][x * WR + wr][t * 16 + r]);
+                const float ref = best == -INFINITY ? 0.0f : best;
                 float4 y = make_float4(0, 0, 0, 0);
                 float sum = 0.0f;
 #pragma unroll
                 for (int x = 0; x < WK; ++x) {
                     const int w = x * WR + wr;
                     const float f = exp2_approx(s_ml[0][w][t * 16 + r] - ref);
-                    const float4 v = *reinterpret_cast<const float4 *>(join + w * kSlice + r * D * 4 + ((c ^ (r & 7) * 2) << 4));
+                    const float4 v = *reinterpret_cast<const float4 *>(join + w * kSlice<D> + r * D * 4 + ((c ^ (r & 7) * 2) << 4));
                     sum = fmaf(f, s_ml[1][w][t * 16 + r], sum);
                     y.x = fmaf(f, v.x, y.x), y.y = fmaf(f, v.y, y.y), y.z = fmaf(f, v.z, y.z), y.w = fmaf(f, v.w, y.w);
                 }
@@ -502,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const TreeAr
                         a.lse[(size_t)token * a.Hkv * a.group + h] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.69314718056f;
                 } else {
                     *reinterpret_cast<float4 *>(a.part + (piece * ROWS + row) * D + 4 * c) = y;
-                    if (c == 0) *reinterpret_cast<float2 *>(a.part_ml + (piece * ROWS + row) * 2) = make_float2(top, sum);
+                    if (c == 0) *reinterpret_cast<float2 *>(a.part_ml + (piece * ROWS + row) * 2) = make_float2(best, sum);
                 }
             }
         }
@@ -513,7 +606,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) tree_kernel(const TreeAr
         }
         left -= kt1 - kt0;
     }
-    copies_wait<0>();
+    if (!kTiled) copies_wait<0>();
+    if (gave_up_word && tid == 0) atomicOr(a.errors, 4u);
 }
 
 // Joins the pieces of the cut sequences: block x the one that begins in CTA x,
@@ -565,30 +659,57 @@ Workspace workspace(int rows, int D) {
     return w;
 }
 
-template <typename E, int D, int WR, int WK, int MT>
-cudaError_t launch_tree(const TreeArgs &a, bool pdl, cudaStream_t s) {
-    constexpr int ROWS = WR * MT * 16, smem = tree_smem_bytes<D, WR, MT>();
-    auto kernel = tree_kernel<E, D, WR, WK, MT>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+// [page][head][row][D] in boxes of 64 columns and 16 rows of a page.
+bool cache_map(CUtensorMap *map, void *base, const fb_kv_cache &c) {
+    const EncodeTiled f = encode_tiled();
+    if (!f) return false;
+    const cuuint64_t row = (cuuint64_t)c.D * 2, head = row * c.page_size;
+    const cuuint64_t dims[4] = {(cuuint64_t)c.D, (cuuint64_t)c.page_size, (cuuint64_t)c.Hkv, (cuuint64_t)c.pages};
+    const cuuint64_t strides[3] = {row, head, head * c.Hkv};
+    const cuuint32_t box[4] = {64, 16, 1, 1}, steps[4] = {1, 1, 1, 1};
+    return f(map, c.t == FB_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims,
+             strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename E, int D, int WR, int WK, int MT, bool kTiled>
+cudaError_t launch_tree(const TreeArgs &a, const fb_kv_cache &cache, bool pdl, cudaStream_t s) {
+    constexpr int ROWS = WR * MT * 16, smem = tree_smem_bytes<D, ROWS>();
+    CUtensorMap k = {}, v = {};
+    if (kTiled && (!cache_map(&k, cache.k, cache) || !cache_map(&v, cache.v, cache))) return cudaErrorInvalidValue;
+    cudaError_t e = allow_shared<tree_kernel<E, D, WR, WK, MT, kTiled>>(smem);
     if (e != cudaSuccess) return e;
     const dim3 grid(sm_count() * kCtasPerSm);
-    e = launch(kernel, grid, dim3(kThreads), smem, s, pdl, a);
+    e = launch(tree_kernel<E, D, WR, WK, MT, kTiled>, grid, dim3(kThreads), smem, s, pdl, a, k, v);
     if (e != cudaSuccess) return e;
     return launch(join_kernel<E, D, ROWS>, dim3(grid.x, ROWS * D / 4 / kThreads), dim3(kThreads), 0, s, true, a);
 }
 
+template <typename E, int D, int WR, int WK, int MT>
+cudaError_t launch_tree_pages(const TreeArgs &a, const fb_kv_cache &cache, bool pdl, cudaStream_t s) {
+    return cache.page_size >= 16 ? launch_tree<E, D, WR, WK, MT, true>(a, cache, pdl, s)
+                                 : launch_tree<E, D, WR, WK, MT, false>(a, cache, pdl, s);
+}
+
 template <typename E, int D>
-cudaError_t launch_tree_rows(const TreeArgs &a, int rows, bool pdl, cudaStream_t s) {
-    if (rows == 16) return launch_tree<E, D, 1, 4, 1>(a, pdl, s);
-    if (rows == 32) return launch_tree<E, D, 1, 4, 2>(a, pdl, s);
-    return launch_tree<E, D, 2, 2, 2>(a, pdl, s);
+cudaError_t launch_tree_rows(const TreeArgs &a, const fb_kv_cache &cache, int rows, bool pdl, cudaStream_t s) {
+    if (rows == 16) return launch_tree_pages<E, D, 1, 4, 1>(a, cache, pdl, s);
+    if (rows == 32) return launch_tree_pages<E, D, 1, 4, 2>(a, cache, pdl, s);
+    return launch_tree_pages<E, D, 2, 2, 2>(a, cache, pdl, s);
 }
 
 }  // namespace
 
 void *attn_errors_address() {
-    void *p = nullptr;
-    return cudaGetSymbolAddress(&p, g_attn_errors) == cudaSuccess ? p : nullptr;
+    static std::atomic<void *> cached[64];   // by device
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+    void *p = cached[dev].load(std::memory_order_relaxed);
+    if (!p) {
+        if (cudaGetSymbolAddress(&p, g_attn_errors) != cudaSuccess) return nullptr;
+        cached[dev].store(p, std::memory_order_relaxed);
+    }
+    return p;
 }
 
 }  // namespace fb
@@ -630,11 +751,13 @@ extern "C" fb_status fb_attn_tree(const void *q, int ldq, int T, int Hq, const f
     a.table_width = table_width, a.ld_table = ld_table, a.max_draft = max_draft;
     a.pages = cache->pages, a.page_shift = log2_of(cache->page_size);
     a.scale_log2 = scale * 1.44269504089f;
+    a.errors = (unsigned int *)attn_errors_address();
+    if (!a.errors) return FB_ERR_CUDA;
     const bool pdl = flags & FB_GEMV_PDL;
     cudaStream_t s = as_stream(stream);
     if (cache->t == FB_F16)
-        return status_of(D == 64 ? launch_tree_rows<__half, 64>(a, rows, pdl, s)
-                                 : launch_tree_rows<__half, 128>(a, rows, pdl, s));
-    return status_of(D == 64 ? launch_tree_rows<__nv_bfloat16, 64>(a, rows, pdl, s)
-                             : launch_tree_rows<__nv_bfloat16, 128>(a, rows, pdl, s));
+        return status_of(D == 64 ? launch_tree_rows<__half, 64>(a, *cache, rows, pdl, s)
+                                 : launch_tree_rows<__half, 128>(a, *cache, rows, pdl, s));
+    return status_of(D == 64 ? launch_tree_rows<__nv_bfloat16, 64>(a, *cache, rows, pdl, s)
+                             : launch_tree_rows<__nv_bfloat16, 128>(a, *cache, rows, pdl, s));
 }

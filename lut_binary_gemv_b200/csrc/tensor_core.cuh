@@ -11,6 +11,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace fb {
 
 // ---- barriers ------------------------------------------------------------------
@@ -70,6 +72,13 @@ __device__ __forceinline__ void tile_copy(uint32_t dst, const CUtensorMap *map, 
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
         ::"r"(dst), "l"(map), "r"(col), "r"(head), "r"(token), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tile_copy4(uint32_t dst, const CUtensorMap *map, int col, int row, int head, int page,
+                                           uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(dst), "l"(map), "r"(col), "r"(row), "r"(head), "r"(page), "r"(bar)
         : "memory");
 }
 // Orders the thread's own writes to shared memory before later reads by copies and matrix instructions.
@@ -224,6 +233,43 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
+}
+
+// ---- host ------------------------------------------------------------------------------------
+
+// The driver's encoder of tensor maps, found once.
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline EncodeTiled encode_tiled() {
+    static std::atomic<EncodeTiled> cached{nullptr};
+    EncodeTiled f = cached.load(std::memory_order_relaxed);
+    if (!f) {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) !=
+                cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            return nullptr;
+        f = reinterpret_cast<EncodeTiled>(p);
+        cached.store(f, std::memory_order_relaxed);
+    }
+    return f;
+}
+
+// Lets a kernel have more than 48 KB of dynamic shared memory; once for each device.
+template <auto Kernel>
+inline cudaError_t allow_shared(int bytes) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 }  // namespace fb

@@ -48,6 +48,9 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kTileKeys = 64;      // keys of a tile, 16 loaded by each warp
 constexpr int kCtasPerSm = 2;
 constexpr int kMinTiles = 2;       // key tiles of a run, at least
+// What starting and ending a piece costs, in key tiles: the list counts every item this much longer.
+template <int MT>
+constexpr int kPieceTiles = MT == 1 ? 3 : 8;
 constexpr float kRescaleLog2 = 8.0f;
 
 __device__ unsigned int g_attn_errors;
@@ -94,12 +97,15 @@ __device__ __forceinline__ Seq sequence(const TreeArgs &a, int s) {
 struct Cursor {
     Seq q;
     int s, item, kt;   // item = key head * row tiles + row tile
+    int64_t pos;       // behind the run's beginning
 };
 
-template <int ROWS>
+template <int ROWS, int kPiece>
 __device__ __forceinline__ void step(const TreeArgs &a, Cursor &c) {
+    ++c.pos;
     if (++c.kt < c.q.tiles) return;
     c.kt = 0;
+    c.pos += kPiece;
     if (++c.item < c.q.row_tiles * a.Hkv) return;
     c.item = 0;
     do {
@@ -179,7 +185,7 @@ template <typename E, int D, int WR, int WK, int MT, bool kTiled>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     tree_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     static_assert(WR * WK == kWarps, "four warps");
-    constexpr int ROWS = WR * MT * 16;
+    constexpr int ROWS = WR * MT * 16, kPiece = kPieceTiles<MT>;
     constexpr int KW = kTileKeys / WK;      // keys a warp multiplies
     constexpr int NT = KW / 8;              // 8-key columns of its scores
     constexpr int CH = D / 8;               // 16-byte chunks of a row
@@ -210,17 +216,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     int64_t total = 0;
     for (int s = lane; s < a.n; s += 32) {
         const Seq q = sequence<ROWS>(a, s);
-        total += (int64_t)q.row_tiles * a.Hkv * q.tiles;
+        total += (int64_t)q.row_tiles * a.Hkv * (q.tiles + kPiece);
         if (q.too_many && blockIdx.x == 0 && warp == 0) atomicOr(a.errors, 2u);
     }
 #pragma unroll
     for (int x = 16; x; x >>= 1) total += __shfl_xor_sync(~0u, total, x);
-    const int64_t run = max((total + gridDim.x - 1) / gridDim.x, (int64_t)kMinTiles);
-    const int64_t begin = run * blockIdx.x;
-    const int64_t mine = min(run, total - begin);
-    int64_t left = mine;
+    const int64_t run = max((total + gridDim.x - 1) / gridDim.x, (int64_t)(kMinTiles + kPiece));
+    const int64_t begin = run * blockIdx.x, span = min(run, total - begin);
     if (tid == 0) a.records[blockIdx.x] = make_int4(0, 0, 0, 0);
-    if (left <= 0) return;
+    if (span <= 0) return;
 
     Cursor at;
     {
@@ -230,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             int64_t w = 0;
             if (base + lane < a.n) {
                 const Seq q = sequence<ROWS>(a, base + lane);
-                w = (int64_t)q.row_tiles * a.Hkv * q.tiles;
+                w = (int64_t)q.row_tiles * a.Hkv * (q.tiles + kPiece);
             }
             int64_t upto = w;
 #pragma unroll
@@ -248,13 +252,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             before += __shfl_sync(~0u, upto, 31);
         }
         at.q = sequence<ROWS>(a, at.s);
-        at.item = (int)((begin - before) / at.q.tiles);
-        at.kt = (int)((begin - before) % at.q.tiles);
+        const int length = at.q.tiles + kPiece;
+        at.item = (int)((begin - before) / length);
+        at.kt = (int)((begin - before) % length) - kPiece;   // an item's tiles come behind its start
+        at.pos = at.kt < 0 ? -at.kt : 0;
+        at.kt = max(at.kt, 0);
     }
 
     // ---- loading: each warp brings in keys 16 warp .. 16 warp + 15 of a tile ----
     Cursor ahead = at;
-    int64_t to_load = left;
     int load_stage = 0;
     // the page of a key position of the cursor's sequence (-1 beyond the table)
     auto page_of = [&](int p) {
@@ -263,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     };
     int page = page_of(ahead.kt * kTileKeys + 16 * warp + (kTiled ? 0 : lane % 16));   // looked up a tile early
     auto load_tile = [&]() {
-        if (to_load > 0) {
+        if (ahead.pos < span) {
             const int hk = ahead.item / ahead.q.row_tiles, keys = ahead.q.len + ahead.q.m;
             const uint32_t k_at = stages + load_stage * kStageBytes<D> + warp * kSlice<D>, v_at = k_at + kHalf;
             const int p0 = ahead.kt * kTileKeys + 16 * warp;
@@ -319,8 +325,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     }
                 }
             }
-            if (--to_load > 0) {
-                step<ROWS>(a, ahead);
+            step<ROWS, kPiece>(a, ahead);
+            if (ahead.pos < span) {
                 page = page_of(ahead.kt * kTileKeys + 16 * warp + (kTiled ? 0 : lane % 16));
             }
         }
@@ -333,10 +339,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // ---- the pieces -------------------------------------------------------------
     int stage = 0, last_stage = 0;
     uint32_t phase = 0;
-    while (left > 0) {
+    while (at.pos < span) {
         const Seq q = at.q;
         const int hk = at.item / q.row_tiles, rt = at.item % q.row_tiles;
-        const int kt0 = at.kt, kt1 = (int)min((int64_t)q.tiles, at.kt + left);
+        const int kt0 = at.kt, kt1 = (int)min((int64_t)q.tiles, at.kt + span - at.pos);
+        const int64_t item_end = at.pos - kt0 + q.tiles;
         const int rows = min(ROWS, q.m * a.group - rt * ROWS);
 
         // the rows' queries and masks (row r: token r / group, head r % group of the key head's)
@@ -476,14 +483,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 }
 
             if (partly) {
-                // values that are not finite: scanned by the warp that loaded them
+                // the warp that loaded the values clears those behind the keys (they may be anything) and
+                // looks for others that are not finite
                 const uint32_t own = stages + stage * kStageBytes<D> + warp * kSlice<D> + kHalf;
+                const int there = q.len + q.m - tile_key - 16 * warp;   // rows of its 16 that are keys
                 bool odd = false;
                 for (int i = lane; i < kHalf / 16; i += 32) {
+                    if (i / 8 % 16 >= there) {
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(own + 16 * i), "r"(0) : "memory");
+                        continue;
+                    }
                     uint4 v;
                     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(own + 16 * i) : "memory");
                     odd |= not_finite<E>(v.x) || not_finite<E>(v.y) || not_finite<E>(v.z) || not_finite<E>(v.w);
                 }
+                writes_before_async();
                 odd = kOwnKeys ? __any_sync(~0u, odd) : __syncthreads_or(odd);
                 if (odd) {
                     for (int kk = 0; kk < KW; ++kk) {
@@ -534,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
             last_stage = stage;
             if (++stage == S) stage = 0, phase ^= 1;
-            step<ROWS>(a, at);
+            step<ROWS, kPiece>(a, at);
         }
 
         // ---- join the key warps through the last tile's place (free until the next tile is
@@ -601,10 +615,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
         // the CTA where a cut sequence begins tells the join where it lies and in which CTA it ends
         if (!whole && kt0 == 0 && tid == 0) {
-            const int64_t end = begin + (mine - left) + q.tiles;
-            a.records[blockIdx.x] = make_int4((int)((end - 1) / run) + 1, q.first, hk * q.row_tiles + rt, rows | q.row_tiles << 16);
+            a.records[blockIdx.x] = make_int4((int)((begin + item_end - 1) / run) + 1, q.first, hk * q.row_tiles + rt, rows | q.row_tiles << 16);
         }
-        left -= kt1 - kt0;
     }
     if (!kTiled) copies_wait<0>();
     if (gave_up_word && tid == 0) atomicOr(a.errors, 4u);

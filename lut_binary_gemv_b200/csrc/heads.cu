@@ -10,9 +10,8 @@
 // loads bound single tokens.  A thread owns 16 elements of a head as two
 // vectors of 8: both halves of 8 pairs, so a rotation never leaves the
 // thread, and a head's sum of squares is log2(D/16) shuffles.  A block takes
-// one token: its angles are computed once (one thread a pair) and kept by
-// each thread for all the heads it visits, since a thread visits the same 8
-// pairs of each.  The angle is reduced in turns in fp64 (pos * inv_freq /
+// one token: its angles are computed once (one thread a pair) and shared by
+// all its heads.  The angle is reduced in turns in fp64 (pos * inv_freq /
 // 2 pi minus its integer), which keeps the error of a position of a million
 // at 1e-10 turns, where fp32 would be off by a hundredth of a turn.
 #include <cuda_bf16.h>
@@ -26,7 +25,7 @@
 namespace fb {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 64;
 
 struct RotateArgs {
     const void *q, *k, *v;
@@ -83,7 +82,7 @@ __device__ __forceinline__ void store8(T *p, const float *f) {
 
 // GL lanes share a head (the power of two at or above D / 16).
 template <typename TI, typename TO, int GL>
-__global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateArgs a) {
+__global__ void __launch_bounds__(kThreads, 16) rotate_kernel(const RotateArgs a) {
     __shared__ float s_cos[128], s_sin[128];
     constexpr int kGroups = kThreads / GL;
     const int tid = threadIdx.x, u = tid % GL, token = blockIdx.x;
@@ -126,24 +125,13 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateArgs a) {
         sincospif(2.0f * (float)(turn - rint(turn)), &s_sin[p], &s_cos[p]);
     }
     __syncthreads();
-    float c[8], s[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = turns ? s_cos[8 * u + i] : 1.0f, s[i] = turns ? s_sin[8 * u + i] : 0.0f;
-
-    float w[16];
-    int kind = -1;   // whose weights w holds: 0 queries, 1 keys, 2 values
     for (int h0 = blockIdx.y * kGroups; h0 < heads; h0 += step, h += step) {   // the same trips for a whole warp
         const bool active = h < heads && in_head;
         float f[16];
         widen(x0, f), widen(x1, f + 8);
         fetch(h + step);
-        const int kd = h < a.Hq ? 0 : h < a.Hq + a.Hkv ? 1 : 2;
+        const int kd = h < a.Hq ? 0 : h < a.Hq + a.Hkv ? 1 : 2;   // queries, keys, values
         const float *wp = kd == 0 ? a.wq : kd == 1 ? a.wk : nullptr;
-        if (active && wp && kd != kind) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = wp[o0 + i], w[8 + i] = wp[o1 + i];
-        }
-        kind = kd;
         float ss = 0.0f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) ss = fmaf(f[i], f[i], ss);
@@ -154,22 +142,22 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateArgs a) {
         if (wp) {
             const float r = rsqrtf(ss / (float)a.D + a.eps);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) f[i] = f[i] * r * w[i];
+            for (int i = 0; i < 8; ++i) f[i] *= r * wp[o0 + i], f[8 + i] *= r * wp[o1 + i];
         }
         int p0 = 16 * u, p1 = 16 * u + 8;
         if (kd < 2) {
             p0 = o0, p1 = o1;
-            if (turns && !a.neighbours) {
+            if (halves) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float x = f[i], y = f[8 + i];
-                    f[i] = x * c[i] - y * s[i], f[8 + i] = y * c[i] + x * s[i];
+                    const float x = f[i], y = f[8 + i], c = s_cos[8 * u + i], s = s_sin[8 * u + i];
+                    f[i] = x * c - y * s, f[8 + i] = y * c + x * s;
                 }
             } else if (turns) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float x = f[2 * i], y = f[2 * i + 1];
-                    f[2 * i] = x * c[i] - y * s[i], f[2 * i + 1] = y * c[i] + x * s[i];
+                    const float x = f[2 * i], y = f[2 * i + 1], c = s_cos[8 * u + i], s = s_sin[8 * u + i];
+                    f[2 * i] = x * c - y * s, f[2 * i + 1] = y * c + x * s;
                 }
             }
         }

@@ -14,6 +14,11 @@ namespace fb {
 constexpr int kMaxTokens = 1 << 24;
 constexpr int kMaxHeads = 1024;
 
+// Outputs are rescaled only when a row's maximum has grown by more than 2^8 since
+// the last time: the sum carries the same factor, and weights up to 2^8 lose
+// nothing in either type.
+constexpr float kRescaleLog2 = 8.0f;
+
 inline int log2_of(int v) {
     int s = 0;
     while ((1 << s) < v) ++s;

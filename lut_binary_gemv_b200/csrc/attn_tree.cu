@@ -37,6 +37,7 @@
 #include <type_traits>
 
 #include "attn_common.cuh"
+#include "attn_seq.cuh"
 #include "fb_internal.cuh"
 #include "tensor_core.cuh"
 
@@ -47,72 +48,11 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTileKeys = 64;      // keys of a tile, 16 loaded by each warp
 constexpr int kCtasPerSm = 2;
-constexpr int kMinTiles = 2;       // key tiles of a run, at least
-// What starting and ending a piece costs, in key tiles: the list counts every item this much longer.
-template <int MT>
-constexpr int kPieceTiles = MT == 1 ? 3 : 8;
-constexpr float kRescaleLog2 = 8.0f;
-
 __device__ unsigned int g_attn_errors;
 
-struct TreeArgs {
-    const void *q, *kc, *vc;
-    void *out;
-    float *lse;
-    const int32_t *table, *lens, *cu;
-    const uint64_t *mask;
-    float *part, *part_ml;
-    int4 *records;
-    unsigned int *errors;
-    int n, T, Hkv, group, ldq, ldo, table_width, ld_table, max_draft, pages, page_shift;
-    float scale_log2;
-};
-
-// One sequence as the kernels see it: its tokens, its keys and its work.
-struct Seq {
-    int first, m, len, tiles, row_tiles;
-    bool too_many;
-};
-
-template <int ROWS>
-__device__ __forceinline__ Seq sequence(const TreeArgs &a, int s) {
-    Seq q;
-    int first = s, end = s + 1;
-    if (a.cu) {
-        first = min(max(a.cu[s], 0), a.T);
-        end = min(max(a.cu[s + 1], first), a.T);
-    }
-    q.first = first;
-    q.too_many = end - first > a.max_draft;
-    q.m = min(end - first, a.max_draft);
-    // more committed keys than the table has room for: one beyond it is enough to make every row NaN
-    const int64_t room = min(((int64_t)a.table_width << a.page_shift) + 1, (int64_t)INT32_MAX - 256);
-    q.len = (int)min((int64_t)max(a.lens[s], 0), room);
-    q.tiles = max(1, (q.len + q.m + kTileKeys - 1) / kTileKeys);
-    q.row_tiles = (q.m * a.group + ROWS - 1) / ROWS;
-    return q;
-}
-
-// A place in the list of key tiles.
-struct Cursor {
-    Seq q;
-    int s, item, kt;   // item = key head * row tiles + row tile
-    int64_t pos;       // behind the run's beginning
-};
-
-template <int ROWS, int kPiece>
-__device__ __forceinline__ void step(const TreeArgs &a, Cursor &c) {
-    ++c.pos;
-    if (++c.kt < c.q.tiles) return;
-    c.kt = 0;
-    c.pos += kPiece;
-    if (++c.item < c.q.row_tiles * a.Hkv) return;
-    c.item = 0;
-    do {
-        if (++c.s >= a.n) return;
-        c.q = sequence<ROWS>(a, c.s);
-    } while (c.q.row_tiles == 0);
-}
+// What starting and ending a piece costs, in key tiles.
+template <int MT>
+constexpr int kPieceTiles = MT == 1 ? 3 : 8;
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool valid) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
@@ -153,19 +93,6 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
 // put it; the eight rows of a matrix load lie in eight different groups of banks.
 __device__ __forceinline__ int chunk_at(int row, int chunk) {
     return (chunk >> 3) * 2048 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
-}
-
-template <typename E>
-__device__ __forceinline__ bool not_finite(uint32_t pair) {
-    constexpr uint32_t e = std::is_same_v<E, __half> ? 0x7C00u : 0x7F80u;
-    return (pair & e) == e || (pair >> 16 & e) == e;
-}
-template <typename E>
-__device__ __forceinline__ uint32_t finite_part(uint32_t pair) {
-    constexpr uint32_t e = std::is_same_v<E, __half> ? 0x7C00u : 0x7F80u;
-    if ((pair & e) == e) pair &= 0xFFFF0000u;
-    if ((pair >> 16 & e) == e) pair &= 0x0000FFFFu;
-    return pair;
 }
 
 template <int D>
@@ -213,51 +140,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     wait_for_previous_kernel();
 
     // ---- this CTA's run of key tiles -----------------------------------------
-    int64_t total = 0;
-    for (int s = lane; s < a.n; s += 32) {
-        const Seq q = sequence<ROWS>(a, s);
-        total += (int64_t)q.row_tiles * a.Hkv * (q.tiles + kPiece);
-        if (q.too_many && blockIdx.x == 0 && warp == 0) atomicOr(a.errors, 2u);
-    }
-#pragma unroll
-    for (int x = 16; x; x >>= 1) total += __shfl_xor_sync(~0u, total, x);
-    const int64_t run = max((total + gridDim.x - 1) / gridDim.x, (int64_t)(kMinTiles + kPiece));
-    const int64_t begin = run * blockIdx.x, span = min(run, total - begin);
-    if (tid == 0) a.records[blockIdx.x] = make_int4(0, 0, 0, 0);
-    if (span <= 0) return;
-
     Cursor at;
-    {
-        int64_t before = 0;
-        int base = 0;
-        for (;; base += 32) {
-            int64_t w = 0;
-            if (base + lane < a.n) {
-                const Seq q = sequence<ROWS>(a, base + lane);
-                w = (int64_t)q.row_tiles * a.Hkv * (q.tiles + kPiece);
-            }
-            int64_t upto = w;
-#pragma unroll
-            for (int x = 1; x < 32; x <<= 1) {
-                const int64_t y = __shfl_up_sync(~0u, upto, x);
-                if (lane >= x) upto += y;
-            }
-            const unsigned past = __ballot_sync(~0u, before + upto > begin);
-            if (past) {
-                const int l = __ffs(past) - 1;
-                at.s = base + l;
-                before += __shfl_sync(~0u, upto - w, l);
-                break;
-            }
-            before += __shfl_sync(~0u, upto, 31);
-        }
-        at.q = sequence<ROWS>(a, at.s);
-        const int length = at.q.tiles + kPiece;
-        at.item = (int)((begin - before) / length);
-        at.kt = (int)((begin - before) % length) - kPiece;   // an item's tiles come behind its start
-        at.pos = at.kt < 0 ? -at.kt : 0;
-        at.kt = max(at.kt, 0);
-    }
+    const Run r = find_run<ROWS, kTileKeys, kPiece>(a, at);
+    if (tid == 0) a.records[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (r.span <= 0) return;
+    const int64_t span = r.span;
 
     // ---- loading: each warp brings in keys 16 warp .. 16 warp + 15 of a tile ----
     Cursor ahead = at;
@@ -325,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     }
                 }
             }
-            step<ROWS, kPiece>(a, ahead);
+            step<ROWS, kTileKeys, kPiece>(a, ahead);
             if (ahead.pos < span) {
                 page = page_of(ahead.kt * kTileKeys + 16 * warp + (kTiled ? 0 : lane % 16));
             }
@@ -548,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
             last_stage = stage;
             if (++stage == S) stage = 0, phase ^= 1;
-            step<ROWS, kPiece>(a, at);
+            step<ROWS, kTileKeys, kPiece>(a, at);
         }
 
         // ---- join the key warps through the last tile's place (free until the next tile is
@@ -615,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
         // the CTA where a cut sequence begins tells the join where it lies and in which CTA it ends
         if (!whole && kt0 == 0 && tid == 0) {
-            a.records[blockIdx.x] = make_int4((int)((begin + item_end - 1) / run) + 1, q.first, hk * q.row_tiles + rt, rows | q.row_tiles << 16);
+            a.records[blockIdx.x] = make_int4((int)((r.begin + item_end - 1) / r.run) + 1, q.first, hk * q.row_tiles + rt, rows | q.row_tiles << 16);
         }
     }
     if (!kTiled) copies_wait<0>();
@@ -656,45 +543,45 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const TreeArgs a) {
             sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718056f;
 }
 
-int rows_of(int most_rows) { return most_rows <= 16 ? 16 : most_rows <= 32 ? 32 : 64; }
+// The rows of a piece, and its CTAs: by the rows that a key head has at most.
+struct Shape {
+    int rows, ctas;
+    bool tiles;   // on the fifth-generation tensor cores
+};
+Shape shape_of(int most_rows, int group, int page_size) {
+    if (most_rows > 32 && 128 % group == 0 && page_size >= 8) return {kTreeTileRows, sm_count(), true};
+    return {most_rows <= 16 ? 16 : most_rows <= 32 ? 32 : 64, sm_count() * kCtasPerSm, false};
+}
 
 // The workspace: the pieces' outputs, their maxima and sums, a record a CTA.
 struct Workspace {
     size_t ml, records, bytes;
 };
-Workspace workspace(int rows, int D) {
-    const size_t ctas = (size_t)sm_count() * kCtasPerSm, pieces = 2 * ctas;
+Workspace workspace(const Shape &sh, int D) {
+    const size_t pieces = 2 * (size_t)sh.ctas;
     Workspace w;
-    w.ml = pieces * rows * D * sizeof(float);
-    w.records = w.ml + pieces * rows * 2 * sizeof(float);
-    w.bytes = w.records + ctas * sizeof(int4);
+    w.ml = pieces * sh.rows * D * sizeof(float);
+    w.records = w.ml + pieces * sh.rows * 2 * sizeof(float);
+    w.bytes = w.records + sh.ctas * sizeof(int4);
     return w;
 }
 
-// [page][head][row][D] in boxes of 64 columns and 16 rows of a page.
-bool cache_map(CUtensorMap *map, void *base, const fb_kv_cache &c) {
-    const EncodeTiled f = encode_tiled();
-    if (!f) return false;
-    const cuuint64_t row = (cuuint64_t)c.D * 2, head = row * c.page_size;
-    const cuuint64_t dims[4] = {(cuuint64_t)c.D, (cuuint64_t)c.page_size, (cuuint64_t)c.Hkv, (cuuint64_t)c.pages};
-    const cuuint64_t strides[3] = {row, head, head * c.Hkv};
-    const cuuint32_t box[4] = {64, 16, 1, 1}, steps[4] = {1, 1, 1, 1};
-    return f(map, c.t == FB_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims,
-             strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+template <typename E, int D, int ROWS>
+cudaError_t launch_join(const TreeArgs &a, int ctas, cudaStream_t s) {
+    return launch(join_kernel<E, D, ROWS>, dim3(ctas, ROWS * D / 4 / kThreads), dim3(kThreads), 0, s, true, a);
 }
 
 template <typename E, int D, int WR, int WK, int MT, bool kTiled>
 cudaError_t launch_tree(const TreeArgs &a, const fb_kv_cache &cache, bool pdl, cudaStream_t s) {
     constexpr int ROWS = WR * MT * 16, smem = tree_smem_bytes<D, ROWS>();
     CUtensorMap k = {}, v = {};
-    if (kTiled && (!cache_map(&k, cache.k, cache) || !cache_map(&v, cache.v, cache))) return cudaErrorInvalidValue;
+    if (kTiled && (!cache_map(&k, cache.k, cache, 16) || !cache_map(&v, cache.v, cache, 16))) return cudaErrorInvalidValue;
     cudaError_t e = allow_shared<tree_kernel<E, D, WR, WK, MT, kTiled>>(smem);
     if (e != cudaSuccess) return e;
     const dim3 grid(sm_count() * kCtasPerSm);
     e = launch(tree_kernel<E, D, WR, WK, MT, kTiled>, grid, dim3(kThreads), smem, s, pdl, a, k, v);
     if (e != cudaSuccess) return e;
-    return launch(join_kernel<E, D, ROWS>, dim3(grid.x, ROWS * D / 4 / kThreads), dim3(kThreads), 0, s, true, a);
+    return launch_join<E, D, ROWS>(a, grid.x, s);
 }
 
 template <typename E, int D, int WR, int WK, int MT>
@@ -704,7 +591,12 @@ cudaError_t launch_tree_pages(const TreeArgs &a, const fb_kv_cache &cache, bool 
 }
 
 template <typename E, int D>
-cudaError_t launch_tree_rows(const TreeArgs &a, const fb_kv_cache &cache, int rows, bool pdl, cudaStream_t s) {
+cudaError_t launch_tree_rows(const TreeArgs &a, const fb_kv_cache &cache, const Shape &sh, bool pdl, cudaStream_t s) {
+    if (sh.tiles) {
+        const cudaError_t e = launch_tree_tiles(a, cache, pdl, s);
+        return e != cudaSuccess ? e : launch_join<E, D, kTreeTileRows>(a, sh.ctas, s);
+    }
+    const int rows = sh.rows;
     if (rows == 16) return launch_tree_pages<E, D, 1, 4, 1>(a, cache, pdl, s);
     if (rows == 32) return launch_tree_pages<E, D, 1, 4, 2>(a, cache, pdl, s);
     return launch_tree_pages<E, D, 2, 2, 2>(a, cache, pdl, s);
@@ -731,7 +623,10 @@ using namespace fb;
 extern "C" size_t fb_attn_tree_workspace_bytes(int Hq, int Hkv, int D, int max_draft) {
     if (Hq < 1 || Hq > kMaxHeads || Hkv < 1 || Hq % Hkv || (D != 64 && D != 128) || max_draft < 1 || max_draft > 64)
         return 0;
-    return workspace(rows_of(max_draft * (Hq / Hkv)), D).bytes;
+    // either shape, whatever the page size
+    const int group = Hq / Hkv, rows = max_draft * group;
+    const size_t a = workspace(shape_of(rows, group, 1), D).bytes, b = workspace(shape_of(rows, group, 8), D).bytes;
+    return a > b ? a : b;
 }
 
 extern "C" fb_status fb_attn_tree(const void *q, int ldq, int T, int Hq, const fb_kv_cache *cache,
@@ -753,8 +648,9 @@ extern "C" fb_status fb_attn_tree(const void *q, int ldq, int T, int Hq, const f
         return FB_ERR_MISALIGNED;
     if (!ws || !aligned(ws, 16) || ws_bytes < fb_attn_tree_workspace_bytes(Hq, cache->Hkv, D, max_draft))
         return FB_ERR_WORKSPACE;
-    const int group = Hq / cache->Hkv, rows = rows_of(max_draft * group);
-    const Workspace w = workspace(rows, D);
+    const int group = Hq / cache->Hkv;
+    const Shape sh = shape_of(max_draft * group, group, cache->page_size);
+    const Workspace w = workspace(sh, D);
     TreeArgs a = {};
     a.q = q, a.kc = cache->k, a.vc = cache->v, a.out = out, a.lse = lse;
     a.table = page_table, a.lens = lens, a.cu = cu_draft, a.mask = mask;
@@ -768,8 +664,8 @@ extern "C" fb_status fb_attn_tree(const void *q, int ldq, int T, int Hq, const f
     const bool pdl = flags & FB_GEMV_PDL;
     cudaStream_t s = as_stream(stream);
     if (cache->t == FB_F16)
-        return status_of(D == 64 ? launch_tree_rows<__half, 64>(a, *cache, rows, pdl, s)
-                                 : launch_tree_rows<__half, 128>(a, *cache, rows, pdl, s));
-    return status_of(D == 64 ? launch_tree_rows<__nv_bfloat16, 64>(a, *cache, rows, pdl, s)
-                             : launch_tree_rows<__nv_bfloat16, 128>(a, *cache, rows, pdl, s));
+        return status_of(D == 64 ? launch_tree_rows<__half, 64>(a, *cache, sh, pdl, s)
+                                 : launch_tree_rows<__half, 128>(a, *cache, sh, pdl, s));
+    return status_of(D == 64 ? launch_tree_rows<__nv_bfloat16, 64>(a, *cache, sh, pdl, s)
+                             : launch_tree_rows<__nv_bfloat16, 128>(a, *cache, sh, pdl, s));
 }

@@ -23,6 +23,7 @@ struct TreeArgs {
     int4 *records;
     unsigned int *errors;
     int n, T, Hkv, group, ldq, ldo, table_width, ld_table, max_draft, pages, page_shift;
+    int whole;   // items are not cut: a run is of items
     float scale_log2;
 };
 
@@ -63,10 +64,10 @@ struct Cursor {
 
 template <int ROWS, int KEYS, int kPiece>
 __device__ __forceinline__ void step(const TreeArgs &a, Cursor &c) {
-    ++c.pos;
+    if (!a.whole) ++c.pos;
     if (++c.kt < c.q.tiles) return;
     c.kt = 0;
-    c.pos += kPiece;
+    c.pos += a.whole ? 1 : kPiece;
     if (++c.item < c.q.row_tiles * a.Hkv) return;
     c.item = 0;
     do {
@@ -86,14 +87,14 @@ __device__ __forceinline__ Run find_run(const TreeArgs &a, Cursor &at) {
     auto weight = [&](int s) {
         const Seq q = sequence<ROWS, KEYS>(a, s);
         if (q.too_many && blockIdx.x == 0) atomicOr(a.errors, 2u);
-        return (int64_t)q.row_tiles * a.Hkv * (q.tiles + kPiece);
+        return (int64_t)q.row_tiles * a.Hkv * (a.whole ? 1 : q.tiles + kPiece);
     };
     int64_t total = 0;
     for (int s = lane; s < a.n; s += 32) total += weight(s);
 #pragma unroll
     for (int x = 16; x; x >>= 1) total += __shfl_xor_sync(~0u, total, x);
     Run r;
-    r.run = max((total + gridDim.x - 1) / gridDim.x, (int64_t)(kMinTiles + kPiece));
+    r.run = max((total + gridDim.x - 1) / gridDim.x, (int64_t)(a.whole ? 1 : kMinTiles + kPiece));
     r.begin = r.run * blockIdx.x, r.span = min(r.run, total - r.begin);
     if (r.span <= 0) return r;
     int64_t before = 0;
@@ -115,6 +116,11 @@ __device__ __forceinline__ Run find_run(const TreeArgs &a, Cursor &at) {
         before += __shfl_sync(~0u, upto, 31);
     }
     at.q = sequence<ROWS, KEYS>(a, at.s);
+    if (a.whole) {
+        at.item = (int)(r.begin - before);
+        at.kt = 0, at.pos = 0;
+        return r;
+    }
     const int length = at.q.tiles + kPiece;
     at.item = (int)((r.begin - before) / length);
     at.kt = (int)((r.begin - before) % length) - kPiece;   // an item's tiles come behind its start

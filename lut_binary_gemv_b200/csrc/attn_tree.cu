@@ -50,6 +50,8 @@ constexpr int kTileKeys = 64;      // keys of a tile, 16 loaded by each warp
 constexpr int kCtasPerSm = 2;
 __device__ unsigned int g_attn_errors;
 
+constexpr int kWholeKeys = 512;    // tables of no more keys: items are not cut
+
 // What starting and ending a piece costs, in key tiles.
 template <int MT>
 constexpr int kPieceTiles = MT == 1 ? 3 : 8;
@@ -142,7 +144,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // ---- this CTA's run of key tiles -----------------------------------------
     Cursor at;
     const Run r = find_run<ROWS, kTileKeys, kPiece>(a, at);
-    if (tid == 0) a.records[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (tid == 0 && !a.whole) a.records[blockIdx.x] = make_int4(0, 0, 0, 0);
+    asm volatile("griddepcontrol.launch_dependents;");   // the join may be made ready; it waits for the end of this grid
     if (r.span <= 0) return;
     const int64_t span = r.span;
 
@@ -229,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     while (at.pos < span) {
         const Seq q = at.q;
         const int hk = at.item / q.row_tiles, rt = at.item % q.row_tiles;
-        const int kt0 = at.kt, kt1 = (int)min((int64_t)q.tiles, at.kt + span - at.pos);
+        const int kt0 = at.kt, kt1 = a.whole ? q.tiles : (int)min((int64_t)q.tiles, at.kt + span - at.pos);
         const int64_t item_end = at.pos - kt0 + q.tiles;
         const int rows = min(ROWS, q.m * a.group - rt * ROWS);
 
@@ -581,7 +584,7 @@ cudaError_t launch_tree(const TreeArgs &a, const fb_kv_cache &cache, bool pdl, c
     const dim3 grid(sm_count() * kCtasPerSm);
     e = launch(tree_kernel<E, D, WR, WK, MT, kTiled>, grid, dim3(kThreads), smem, s, pdl, a, k, v);
     if (e != cudaSuccess) return e;
-    return launch_join<E, D, ROWS>(a, grid.x, s);
+    return a.whole ? cudaSuccess : launch_join<E, D, ROWS>(a, grid.x, s);
 }
 
 template <typename E, int D, int WR, int WK, int MT>
@@ -661,6 +664,8 @@ extern "C" fb_status fb_attn_tree(const void *q, int ldq, int T, int Hq, const f
     a.scale_log2 = scale * 1.44269504089f;
     a.errors = (unsigned int *)attn_errors_address();
     if (!a.errors) return FB_ERR_CUDA;
+    // Where every sequence is short, cutting gains less than the second launch costs.
+    a.whole = !sh.tiles && (int64_t)table_width * cache->page_size <= kWholeKeys;
     const bool pdl = flags & FB_GEMV_PDL;
     cudaStream_t s = as_stream(stream);
     if (cache->t == FB_F16)

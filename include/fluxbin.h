@@ -256,7 +256,7 @@ FB_API fb_status fb_gemv_launch_plan(const fb_weights *W, int batch, unsigned fl
  * GEMV gave up its bounded wait for the row partials of its cluster; the rows
  * it owns were written as NaN; bit 1: fb_attn_tree met a page outside the
  * cache or a sequence of too many drafted tokens; bit 2: a CTA of an attention
- * call gave up a bounded wait, its rows were not written), and clears them
+ * call gave up a bounded wait, its rows hold no result), and clears them
  * when clear != 0.  Returns
  * FB_ERR_INVALID_VALUE for a null flags, FB_ERR_CUDA if the device reports an
  * error, else FB_OK. */
@@ -365,7 +365,8 @@ FB_API fb_status fb_qk_norm_rope(const fb_heads *in, const fb_heads *out, const 
  * Rows of no sequence keep their contents.  What lies outside a sequence, and
  * later tokens within it, never reaches a row, whatever the values (NaN and
  * infinity included).  The weights p are rounded to in->t before they meet v
- * (the tensor cores take operands of one type), their sum is of fp32 values. */
+ * (the tensor cores take operands of one type), their sum is of fp32 values.
+ * An infinite or NaN score among those a row sees makes the row NaN. */
 FB_API fb_status fb_attn_prompt(const fb_heads *in, const int32_t *cu_seqlens, int n, float scale, void *out, int ldo,
                                 float *lse, unsigned flags, void *stream);
 
@@ -388,8 +389,10 @@ FB_API fb_status fb_attn_prompt(const fb_heads *in, const int32_t *cu_seqlens, i
  * among the keys that a row sees gives NaN in that row, and a sequence of
  * more than max_draft tokens leaves those behind them unwritten; both raise
  * bit 1 of fb_device_errors, and no memory outside the cache is read.  Tokens
- * of no sequence keep their contents.  The weights are rounded as in
- * fb_attn_prompt.
+ * of no sequence keep their contents.  Where a key head has more than 32 rows
+ * (max_draft * Hq / Hkv), Hq / Hkv divides 128 and page_size >= 8, the weights
+ * are rounded as in fb_attn_prompt; otherwise they keep 2^-16 of their size,
+ * and an infinite value among the committed keys gives infinity or NaN.
  * ws: fb_attn_tree_workspace_bytes bytes, 16-byte aligned, for the partial
  * results of sequences split over several CTAs; its contents need not be
  * set up and mean nothing afterwards, but calls that may run at the same

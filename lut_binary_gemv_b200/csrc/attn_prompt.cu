@@ -37,7 +37,8 @@ using namespace fb;
 extern "C" fb_status fb_attn_prompt(const fb_heads *in, const int32_t *cu_seqlens, int n, float scale, void *out,
                                     int ldo, float *lse, unsigned flags, void *stream) {
     if (!in || (flags & ~FB_GEMV_PDL) || !valid_heads(*in) || !in->q || !in->k || !in->v || !out || !cu_seqlens ||
-        n < 1 || n > kMaxTokens || ldo < in->Hq * in->D || !(scale > 0.0f) || scale > 3e38f)
+        n < 1 || n > kMaxTokens || ldo < in->Hq * in->D || !(scale > 0.0f) || scale > 1e38f ||
+        out == in->q || out == in->k || out == in->v)
         return FB_ERR_INVALID_VALUE;
     if (in->t == FB_F32 || (in->D != 64 && in->D != 128)) return FB_ERR_UNSUPPORTED;
     if (!aligned(in->q, 16) || !aligned(in->k, 16) || !aligned(in->v, 16) || !aligned(out, 16) || in->ldq % 8 ||

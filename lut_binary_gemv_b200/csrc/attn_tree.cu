@@ -355,7 +355,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                         for (int j = 0; j < D / 8; ++j) o[t][j][2 * half] *= f, o[t][j][2 * half + 1] *= f;
                     }
             }
-            uint32_t pa[MT][NT / 2][4];
+            // The weights meet the values as two operands, the rounded weight and what the rounding left: beside the
+            // stream of keys the second product costs nothing for up to 16 rows and 3% for up to 32, and the weights
+            // lose no more than 2^-16 of their size.
+            uint32_t pa[MT][NT / 2][4], pr[MT][NT / 2][4];
 #pragma unroll
             for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -367,7 +370,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                         const float p0 = exp2_approx(fmaf(s[t][j][2 * half], a.scale_log2, -ref));
                         const float p1 = exp2_approx(fmaf(s[t][j][2 * half + 1], a.scale_log2, -ref));
                         sum += p0 + p1;
-                        pa[t][j / 2][(j % 2) * 2 + half] = pack2<E>(p0, p1);
+                        const uint32_t near = pack2<E>(p0, p1);
+                        pa[t][j / 2][(j % 2) * 2 + half] = near;
+                        const float2 had = unpack2<E>(near);
+                        pr[t][j / 2][(j % 2) * 2 + half] = pack2<E>(p0 - had.x, p1 - had.y);
                     }
                     l[t][half] += sum;
                 }
@@ -432,8 +438,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     uint32_t vb[4];
                     ldmatrix4_trans(vb, values_at + c * kSlice<D> + chunk_at(lane % 16, 2 * d + lane / 16));
 #pragma unroll
-                    for (int t = 0; t < MT; ++t)
+                    for (int t = 0; t < MT; ++t) {
                         mma<E>(o[t][2 * d], pa[t][c], vb[0], vb[1]), mma<E>(o[t][2 * d + 1], pa[t][c], vb[2], vb[3]);
+                        mma<E>(o[t][2 * d], pr[t][c], vb[0], vb[1]), mma<E>(o[t][2 * d + 1], pr[t][c], vb[2], vb[3]);
+                    }
                 }
 
             last_stage = stage;
@@ -640,7 +648,7 @@ extern "C" fb_status fb_attn_tree(const void *q, int ldq, int T, int Hq, const f
     if (!q || !cache || !page_table || !lens || !out || (flags & ~FB_GEMV_PDL) || !valid_cache(*cache) || T < 1 ||
         T > kMaxTokens || Hq < 1 || Hq > kMaxHeads || Hq % cache->Hkv || n < 1 || n > 65536 || table_width < 1 ||
         ld_table < table_width ||
-        max_draft < 1 || max_draft > 64 || (!cu_draft && T != n) || !(scale > 0.0f) || scale > 3e38f)
+        max_draft < 1 || max_draft > 64 || (!cu_draft && T != n) || !(scale > 0.0f) || scale > 1e38f || out == q)
         return FB_ERR_INVALID_VALUE;
     const int D = cache->D;
     if (ldq < (int64_t)Hq * D || ldo < (int64_t)Hq * D) return FB_ERR_INVALID_VALUE;

@@ -70,7 +70,10 @@ def test_rope_refusals(L, args, status):
     assert rope(L, **args) == status
 
 
-def prompt(L, h=None, cu=FAKE, n=2, scale=0.1, out=FAKE, ldo=1024, lse=FAKE, flags=0):
+OUT = 0x20000
+
+
+def prompt(L, h=None, cu=FAKE, n=2, scale=0.1, out=OUT, ldo=1024, lse=FAKE, flags=0):
     h = h or heads()
     return L.fb_attn_prompt(C.byref(h), cu, n, scale, out, ldo, lse, flags, None)
 
@@ -81,8 +84,9 @@ def prompt(L, h=None, cu=FAKE, n=2, scale=0.1, out=FAKE, ldo=1024, lse=FAKE, fla
     (dict(cu=None), INVALID), (dict(n=0), INVALID), (dict(out=None), INVALID), (dict(ldo=1016), INVALID),
     (dict(scale=0.0), INVALID), (dict(scale=-0.1), INVALID), (dict(scale=math.nan), INVALID),
     (dict(scale=math.inf), INVALID), (dict(flags=2), INVALID), (dict(flags=0x10), INVALID),
+    (dict(scale=2e38), INVALID), (dict(out=FAKE), INVALID),
     (dict(h=heads(t=F32)), UNSUPPORTED), (dict(h=heads(D=96)), UNSUPPORTED),
-    (dict(h=heads(q=FAKE + 8)), MISALIGNED), (dict(h=heads(ldv=260)), MISALIGNED), (dict(out=FAKE + 8), MISALIGNED),
+    (dict(h=heads(q=FAKE + 8)), MISALIGNED), (dict(h=heads(ldv=260)), MISALIGNED), (dict(out=OUT + 8), MISALIGNED),
     (dict(ldo=1028), MISALIGNED), (dict(cu=FAKE + 1), MISALIGNED), (dict(lse=FAKE + 2), MISALIGNED),
 ])
 def test_prompt_refusals(L, args, status):
@@ -90,7 +94,7 @@ def test_prompt_refusals(L, args, status):
 
 
 def tree(L, q=FAKE, ldq=1024, T=4, Hq=8, cache=None, table=FAKE, width=8, ld=8, lens=FAKE, cu=FAKE, n=2, most=3,
-         mask=FAKE, scale=0.1, out=FAKE, ldo=1024, lse=FAKE, ws=FAKE, ws_bytes=1 << 30, flags=0):
+         mask=FAKE, scale=0.1, out=OUT, ldo=1024, lse=FAKE, ws=FAKE, ws_bytes=1 << 30, flags=0):
     kv = cache or kv_cache()
     return L.fb_attn_tree(q, ldq, T, Hq, C.byref(kv), table, width, ld, lens, cu, n, most, mask, scale, out, ldo, lse,
                           ws, ws_bytes, flags, None)
@@ -104,7 +108,8 @@ def tree(L, q=FAKE, ldq=1024, T=4, Hq=8, cache=None, table=FAKE, width=8, ld=8, 
     (dict(scale=math.nan), INVALID), (dict(flags=2), INVALID), (dict(cache=kv_cache(t=F32)), INVALID),
     (dict(cache=kv_cache(page_size=0)), INVALID), (dict(cache=kv_cache(v=None)), INVALID),
     (dict(cache=kv_cache(D=96), ldq=1024), UNSUPPORTED),
-    (dict(q=FAKE + 8), MISALIGNED), (dict(out=FAKE + 4), MISALIGNED), (dict(ldq=1028), MISALIGNED),
+    (dict(out=FAKE), INVALID), (dict(scale=math.inf), INVALID),
+    (dict(q=FAKE + 8), MISALIGNED), (dict(out=OUT + 4), MISALIGNED), (dict(ldq=1028), MISALIGNED),
     (dict(table=FAKE + 2), MISALIGNED), (dict(lens=FAKE + 1), MISALIGNED), (dict(cu=FAKE + 2), MISALIGNED),
     (dict(mask=FAKE + 4), MISALIGNED), (dict(lse=FAKE + 1), MISALIGNED),
     (dict(ws=None), WORKSPACE), (dict(ws=FAKE + 8), WORKSPACE), (dict(ws_bytes=0), WORKSPACE),
@@ -118,6 +123,26 @@ def test_tree_workspace_bytes(L):
     for bad in [(0, 1, 128, 1), (8, 3, 128, 1), (8, 0, 128, 1), (8, 8, 96, 1), (8, 8, 64, 0), (8, 8, 64, 65),
                 (2048, 8, 64, 1)]:
         assert L.fb_attn_tree_workspace_bytes(*bad) == 0
+
+
+def test_tree_workspace_follows_the_rows(L):
+    sizes = [L.fb_attn_tree_workspace_bytes(64, 8, 128, m) for m in (1, 2, 4, 5, 64)]
+    assert sizes[0] == sizes[1] < sizes[2] < sizes[3] == sizes[4]        # up to 16, 32 and more rows a key head
+    assert L.fb_attn_tree_workspace_bytes(64, 8, 64, 1) < sizes[0]
+    # a workspace one byte short is refused, whatever the page size
+    for size, page in ((sizes[4], 16), (sizes[4], 64)):
+        c = kv_cache(Hkv=8, page_size=page)
+        args = dict(q=FAKE, ldq=8192, T=64, Hq=64, cache=c, n=2, most=64, ldo=8192)
+        assert tree(L, **args, ws_bytes=0) == WORKSPACE
+        assert tree(L, **args, ws=FAKE + 4, ws_bytes=size) == WORKSPACE
+
+
+def test_struct_bytes_match_the_structs():
+    assert fb._HEADS.size == C.sizeof(fb.FbHeadsStruct) and fb._CACHE.size == C.sizeof(fb.FbKvCacheStruct)
+    h = fb.FbHeadsStruct(q=1, k=2, v=3, t=4, T=5, Hq=6, Hkv=7, D=8, ldq=9, ldk=10, ldv=11)
+    assert bytes(h) == fb._HEADS.pack(*range(1, 12))
+    c = fb.FbKvCacheStruct(k=1, v=2, t=3, pages=4, page_size=5, Hkv=6, D=7)
+    assert bytes(c) == fb._CACHE.pack(*range(1, 8))
 
 
 def test_binding_refuses_what_is_not_on_the_gpu_or_shaped_otherwise():

@@ -304,6 +304,37 @@ def test_prompt_clamps_offsets_outside_the_tokens():
     assert torch.equal(fb.fb_attn_prompt(q, k, v, wild), ref)
 
 
+def test_prompt_that_starts_behind_the_first_token():
+    q, k, v, cu, cud = prompt_inputs([60, 9], 2, 2, 128, torch.float16, seed=14)
+    out = torch.full_like(q, 3.0)
+    fb.fb_attn_prompt(q, k, v, torch.tensor([11, 60], dtype=torch.int32, device=DEV), out=out)
+    check_attention(out, None, prompt_refs(q, k, v, [11, 60], 128 ** -0.5), 128, torch.float16, "late")
+    assert bool((out[:11] == 3.0).all()) and bool((out[60:] == 3.0).all())
+
+
+def test_prompt_many_short_sequences_and_heads():
+    rng = np.random.default_rng(5)
+    lens = rng.integers(0, 40, 300).tolist()
+    q, k, v, cu, cud = prompt_inputs(lens, 40, 8, 64, torch.bfloat16, seed=15)
+    lse = torch.empty(q.shape[0], 40, device=DEV)
+    out = fb.fb_attn_prompt(q, k, v, cud, lse=lse)
+    check_attention(out, lse, prompt_refs(q, k, v, cu, 64 ** -0.5, heads=[0, 17, 39]), 64, torch.bfloat16, "short")
+
+
+def test_prompts_on_two_streams_at_once():
+    cases = [prompt_inputs([1500], 8, 2, 128, torch.bfloat16, seed=s) for s in (16, 17)]
+    refs = [fb.fb_attn_prompt(q, k, v, cud) for q, k, v, _, cud in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = []
+    for _ in range(3):
+        for (q, k, v, _, cud), s in zip(cases, streams):
+            with torch.cuda.stream(s):
+                outs.append(fb.fb_attn_prompt(q, k, v, cud))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, refs[i % 2]) for i, o in enumerate(outs)) and fb.fb_device_errors() == 0
+
+
 def test_prompt_side_stream_and_graph():
     q, k, v, cu, cud = prompt_inputs([300, 50], 4, 2, 128, torch.bfloat16, seed=3)
     ref = fb.fb_attn_prompt(q, k, v, cud)
@@ -404,6 +435,12 @@ TREES = [
     ([200] * 40, [1] * 40, 6, 2, 128, 4, torch.float16),
     ([6000], [2], 16, 2, 128, 64, torch.bfloat16),
     ([9, 2000, 31], [31, 7, 1], 40, 8, 64, 1024, torch.float16),
+    # more than 32 rows a key head
+    ([700, 5, 1300, 127], [64, 40, 9, 1], 16, 2, 128, 8, torch.bfloat16),
+    ([129, 0], [64, 3], 64, 1, 64, 64, torch.float16),
+    ([0, 2500, 128], [33, 64, 50], 8, 8, 128, 16, torch.float16),
+    ([9000], [64], 8, 1, 128, 256, torch.bfloat16),
+    ([300, 64], [7, 64], 128, 1, 64, 128, torch.bfloat16),
 ]
 
 
@@ -438,39 +475,91 @@ def test_tree_masks_that_leave_nothing_or_holes():
         assert not out[row].any() and bool((lse[row] == -float("inf")).all())
 
 
+# up to 16 rows a key head, up to 32, more by each path
+@pytest.mark.parametrize("Hq,page_size", [(2, 16), (2, 4), (8, 16), (8, 4)])
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
-def test_tree_special_values_reach_only_rows_that_see_them(value):
-    c = tree_inputs([50], [20], 8, 2, 128, 16, torch.bfloat16, seed=5)
+def test_tree_special_values_reach_only_rows_that_see_them(value, Hq, page_size):
+    c = tree_inputs([50], [20], Hq, 2, 128, page_size, torch.bfloat16, seed=5)
     ref, _ = tree_call(c)
     j = 7
     p = 50 + j
-    page, row = int(c["table"][0, p // 16]), p % 16
+    page, row = int(c["table"][0, p // page_size]), p % page_size
     c["v"][page, 1, row, 5] = value
     got, _ = tree_call(c)
-    hit = torch.zeros(20, 8, 128, dtype=torch.bool, device=DEV)
+    hit = torch.zeros(20, Hq, 128, dtype=torch.bool, device=DEV)
     for i in range(20):
         if c["masks"][i] >> j & 1:
-            hit[i, 4:, 5] = True
+            hit[i, Hq // 2:, 5] = True
     assert torch.equal(got[~hit], ref[~hit])
     assert bool((torch.isnan(got[hit]) if value != value else got[hit] == value).all())
 
 
 @pytest.mark.parametrize("where", ["page", "negative", "width"])
-def test_tree_bad_pages_give_nan_and_an_error_bit(where):
-    c = tree_inputs([300, 20, 45], [2, 1, 1], 8, 2, 64, 16, torch.float16, seed=6)
+@pytest.mark.parametrize("Hq,page_size", [(8, 16), (8, 8), (64, 16), (64, 4)])
+def test_tree_bad_pages_give_nan_and_an_error_bit(where, Hq, page_size):
+    c = tree_inputs([300, 20, 45], [2, 1, 1], Hq, 2, 64, page_size, torch.float16, seed=6)
     ref, _ = tree_call(c)
     assert fb.fb_device_errors() == 0
     if where == "width":
-        c["table"] = np.ascontiguousarray(c["table"][:, :12])             # 192 positions of 302
+        c["table"] = np.ascontiguousarray(c["table"][:, :192 // page_size])   # 192 positions of 302
     else:
         c["table"][0, 3] = c["k"].shape[0] if where == "page" else -7
     out, lse = tree_call(c, None)
-    ok, _ = tree_call({**c, "table": np.where(c["table"] < 0, 0, np.minimum(c["table"], c["k"].shape[0] - 1))}, None) \
-        if where != "width" else (None, None)
-    assert fb.fb_device_errors() & 2 and fb.fb_device_errors() == 0
+    assert fb.fb_device_errors() == 2 and fb.fb_device_errors() == 0
     assert bool(torch.isnan(out[:2]).all()) and bool(torch.isnan(lse[:2]).all())
     assert bool(torch.isfinite(out[2:]).all())
     assert torch.equal(out[2:], ref[2:])
+
+
+def test_tree_bad_page_among_the_drafts_reaches_only_rows_that_see_it():
+    c = tree_inputs([64], [20], 8, 2, 128, 8, torch.bfloat16, seed=12)
+    ref, _ = tree_call(c)
+    c["table"][0, 9] = -5                                                 # drafted tokens 8 to 15
+    got, lse = tree_call(c)
+    assert fb.fb_device_errors() == 2
+    for i in range(20):
+        if c["masks"][i] >> 8 & 0xFF:
+            assert bool(torch.isnan(got[i]).all()) and bool(torch.isnan(lse[i]).all())
+        else:
+            assert torch.equal(got[i], ref[i])
+
+
+@pytest.mark.parametrize("Hq", [4, 64])
+def test_tree_lengths_beyond_every_bound(Hq):
+    c = tree_inputs([100, 30, 7], [1, 2, 1], Hq, 2, 64, 16, torch.bfloat16, seed=13)
+    ref, _ = tree_call(c)
+    c["lens"] = [2 ** 31 - 1, 30, -4]
+    out, _ = tree_call(c)
+    assert fb.fb_device_errors() == 2
+    assert bool(torch.isnan(out[0]).all()) and torch.equal(out[1:3], ref[1:3])
+    c["lens"] = [100, 30, 0]                                              # a negative length is none
+    again, _ = tree_call(c)
+    assert torch.equal(again[3], out[3]) and fb.fb_device_errors() == 0
+
+
+@pytest.mark.parametrize("page_size,Hq,drafts", [(64, 8, 1), (4, 8, 1), (64, 8, 20)])
+def test_tree_and_rope_in_a_cache_past_32_bits(page_size, Hq, drafts):
+    # 2.4e9 elements of keys and as many of values; the sequence lies in the last pages
+    Hkv, D = 8, 128
+    pages = 2_400_000_000 // (Hkv * page_size * D)
+    if torch.cuda.mem_get_info()[0] < 14 * 10 ** 9:
+        pytest.skip("needs 14 GB")
+    g = gen(31)
+    k, v = (torch.empty(pages, Hkv, page_size, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    T = 70 + drafts
+    need = -(-T // page_size)
+    table = torch.arange(pages - need, pages, dtype=torch.int32, device=DEV).flip(0)[None].contiguous()
+    at = torch.arange(T, device=DEV)
+    slots = (table[0, at // page_size].long() * page_size + at % page_size).to(torch.int32)
+    q, kk, vv = (normal(g, T, H, D, dtype=torch.bfloat16) for H in (Hkv, Hkv, Hkv))
+    qr, kr, _ = fb.fb_qk_norm_rope(q, kk, vv, at.to(torch.int32), fb.rope_frequencies(D))
+    fb.fb_qk_norm_rope(q, kk, vv, at.to(torch.int32), fb.rope_frequencies(D), cache=(k, v), slots=slots)
+    cu = torch.tensor([0, drafts], dtype=torch.int32, device=DEV)
+    lens = torch.tensor([70], dtype=torch.int32, device=DEV)
+    out = fb.fb_attn_tree(qr[70:], (k, v), table, lens, cu, drafts)
+    want = fb.fb_attn_prompt(qr, kr, vv, torch.tensor([0, T], dtype=torch.int32, device=DEV))[70:]
+    assert fb.fb_device_errors() == 0
+    assert (out.float() - want.float()).abs().max() <= 4 * HALF[torch.bfloat16] * vv.abs().max()
 
 
 def test_tree_counts_above_max_draft():
@@ -504,18 +593,20 @@ def test_tree_rows_of_no_sequence_and_strided_rows():
     assert bool((lse[:2] == 11.0).all()) and bool((lse[7:] == 11.0).all())
 
 
-def test_tree_graphs_with_a_workspace_each():
-    c = tree_inputs([4000, 900], [1, 1], 16, 2, 128, 64, torch.bfloat16, seed=9)
+@pytest.mark.parametrize("drafts", [1, 30])
+def test_tree_graphs_with_a_workspace_each(drafts):
+    c = tree_inputs([4000, 900], [drafts, drafts], 16, 2, 128, 64, torch.bfloat16, seed=9)
+    cu = torch.tensor(c["cu"], device=DEV)
     table, lens = torch.tensor(c["table"], device=DEV), torch.tensor(c["lens"], dtype=torch.int32, device=DEV)
-    ref = fb.fb_attn_tree(c["q"], (c["k"], c["v"]), table, lens)
+    ref = fb.fb_attn_tree(c["q"], (c["k"], c["v"]), table, lens, cu, drafts)
     outs = [torch.empty_like(ref) for _ in range(2)]
-    wss = [torch.full((fb.fb_attn_tree_workspace_bytes(16, 2, 128),), 255, dtype=torch.uint8, device=DEV)
+    wss = [torch.full((fb.fb_attn_tree_workspace_bytes(16, 2, 128, drafts),), 255, dtype=torch.uint8, device=DEV)
            for _ in range(2)]
     graphs = []
     for o, w in zip(outs, wss):
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
-            fb.fb_attn_tree(c["q"], (c["k"], c["v"]), table, lens, out=o, ws=w)
+            fb.fb_attn_tree(c["q"], (c["k"], c["v"]), table, lens, cu, drafts, out=o, ws=w)
         graphs.append(graph)
     streams = [torch.cuda.Stream() for _ in graphs]
     torch.cuda.synchronize()
@@ -528,7 +619,7 @@ def test_tree_graphs_with_a_workspace_each():
     lens.copy_(torch.tensor([1234, 8], dtype=torch.int32, device=DEV))
     graphs[0].replay()
     torch.cuda.synchronize()
-    assert torch.equal(outs[0], fb.fb_attn_tree(c["q"], (c["k"], c["v"]), table, lens))
+    assert torch.equal(outs[0], fb.fb_attn_tree(c["q"], (c["k"], c["v"]), table, lens, cu, drafts))
 
 
 def test_prompt_and_tree_agree_on_a_chain():

@@ -252,12 +252,9 @@ FB_API fb_status fb_gemv_group_scales(const fb_weights *W, int G, const void *x,
 FB_API fb_status fb_gemv_launch_plan(const fb_weights *W, int batch, unsigned flags, int sms, int *out);
 
 /* fb_device_errors: synchronises the current device, then stores in *flags
- * the error bits kernels have raised since the last clear (bit 0: a CTA of a
- * GEMV gave up its bounded wait for the row partials of its cluster; the rows
- * it owns were written as NaN; bit 1: fb_attn_tree met a page outside the
- * cache or a sequence of too many drafted tokens; bit 2: a CTA of an attention
- * call gave up a bounded wait, its rows hold no result), and clears them
- * when clear != 0.  Returns
+ * the error bits GEMV kernels have raised since the last clear (bit 0: a CTA
+ * gave up its bounded wait for the row partials of its cluster; the rows it
+ * owns were written as NaN), and clears them when clear != 0.  Returns
  * FB_ERR_INVALID_VALUE for a null flags, FB_ERR_CUDA if the device reports an
  * error, else FB_OK. */
 FB_API fb_status fb_device_errors(unsigned int *flags, int clear);
@@ -388,7 +385,7 @@ FB_API fb_status fb_attn_prompt(const fb_heads *in, const int32_t *cu_seqlens, i
  * there.  A page outside [0, pages), or a position beyond table_width pages,
  * among the keys that a row sees gives NaN in that row, and a sequence of
  * more than max_draft tokens leaves those behind them unwritten; both raise
- * bit 1 of fb_device_errors, and no memory outside the cache is read.  Tokens
+ * bit 0 of fb_attn_errors, and no memory outside the cache is read.  Tokens
  * of no sequence keep their contents.  Where a key head has more than 32 rows
  * (max_draft * Hq / Hkv), Hq / Hkv divides 128 and page_size >= 8, the weights
  * are rounded as in fb_attn_prompt; otherwise they keep 2^-16 of their size,
@@ -403,6 +400,12 @@ FB_API fb_status fb_attn_tree(const void *q, int ldq, int T, int Hq, const fb_kv
                               const int32_t *page_table, int table_width, int ld_table, const int32_t *lens,
                               const int32_t *cu_draft, int n, int max_draft, const uint64_t *mask, float scale, void *out, int ldo, float *lse,
                               void *ws, size_t ws_bytes, unsigned flags, void *stream);
+
+/* fb_attn_errors: as fb_device_errors, of the attention calls' kernels.  Bit 0:
+ * fb_attn_tree met a page outside the cache, or a sequence of more drafted
+ * tokens than max_draft.  Bit 1: a CTA gave up a bounded wait (about two
+ * seconds); its rows hold no result. */
+FB_API fb_status fb_attn_errors(unsigned int *flags, int clear);
 
 /* Human-readable name of a status code (static string). */
 FB_API const char *fb_status_string(fb_status s);

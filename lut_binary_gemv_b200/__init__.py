@@ -28,7 +28,7 @@ __all__ = [
     "fb_gemv_batched", "fb_status_string", "fb_gemv_launch_plan", "fb_gemv_grouped", "fb_device_errors",
     "fb_fit_saliency", "fb_fit_base", "fit", "fb_gemv_group_scales",
     "FB_ROPE_NEIGHBOURS", "rope_frequencies", "fb_qk_norm_rope", "fb_attn_prompt", "fb_attn_tree",
-    "fb_attn_tree_workspace_bytes",
+    "fb_attn_tree_workspace_bytes", "fb_attn_errors",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -110,6 +110,7 @@ def lib() -> C.CDLL:
             "fb_qk_norm_rope": (I, [H, H, P, P, I, P, P, F, KV, P, U, P]),
             "fb_attn_prompt": (I, [H, P, I, F, P, I, P, U, P]),
             "fb_attn_tree_workspace_bytes": (S, [I, I, I, I]),
+            "fb_attn_errors": (I, [P, I]),
             "fb_attn_tree": (I, [P, I, I, I, KV, P, I, I, P, P, I, I, P, F, P, I, P, P, S, U, P]),
             "fb_status_string": (C.c_char_p, [I]),
             "fb_abi_version": (I, []),
@@ -608,3 +609,11 @@ def fb_attn_tree(q: torch.Tensor, cache, page_table: torch.Tensor, lens: torch.T
                _head_rows(out, "out", dev, qs, t), _flat(lse, "lse", torch.float32, T * Hq, dev), ws.data_ptr(),
                ws.numel() * ws.element_size(), flags), "fb_attn_tree")
     return out
+
+
+def fb_attn_errors(clear: bool = True) -> int:
+    """Error bits raised by attention kernels since the last clear (synchronises the device): 1, a page outside the
+    cache or too many drafted tokens; 2, a wait that gave up."""
+    flags = C.c_uint(0)
+    _check(lib().fb_attn_errors(C.cast(C.byref(flags), C.c_void_p), int(clear)), "fb_attn_errors")
+    return flags.value

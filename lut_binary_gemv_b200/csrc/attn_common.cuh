@@ -19,6 +19,11 @@ constexpr int kMaxHeads = 1024;
 // nothing in either type.
 constexpr float kRescaleLog2 = 8.0f;
 
+// Device address of the word in which the attention kernels raise the bits of
+// fb_attn_errors, on the current device (null on a CUDA error).
+void *attn_errors_address();
+constexpr unsigned kErrorInput = 1u, kErrorWait = 2u;
+
 inline int log2_of(int v) {
     int s = 0;
     while ((1 << s) < v) ++s;

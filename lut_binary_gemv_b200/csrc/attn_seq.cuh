@@ -86,7 +86,7 @@ __device__ __forceinline__ Run find_run(const TreeArgs &a, Cursor &at) {
     const int lane = threadIdx.x % 32;
     auto weight = [&](int s) {
         const Seq q = sequence<ROWS, KEYS>(a, s);
-        if (q.too_many && blockIdx.x == 0) atomicOr(a.errors, 2u);
+        if (q.too_many && blockIdx.x == 0) atomicOr(a.errors, kErrorInput);
         return (int64_t)q.row_tiles * a.Hkv * (a.whole ? 1 : q.tiles + kPiece);
     };
     int64_t total = 0;

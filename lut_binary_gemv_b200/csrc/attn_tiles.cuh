@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     const uint32_t to = ring + place * kTileBytes<D> + lane * box * 128, full = bar(bars.full[place]);
                     const uint32_t bytes = __popc(__ballot_sync(~0u, good)) * box * D * 2;
                     if (wanted && !good) {   // no such page: the rows that see it become NaN
-                        atomicOr(a.errors, 2u);
+                        atomicOr(a.errors, kErrorInput);
                         for (int x = 0; x < D / 64; ++x)
                             for (int i = 0; i < box * 128; i += 16)
                                 asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(to + x * (kTile * 128) + i),
@@ -684,7 +684,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         // copies and products that were under way land in this CTA's memory: give them time before it is reused
         const uint64_t start = now_ns();
         while (now_ns() - start < 20000000ull) __nanosleep(1000);
-        if (tid == 0) atomicOr(a.errors, 4u);
+        if (tid == 0) atomicOr(a.errors, kErrorWait);
         __syncthreads();
     }
     if (warp == 9) tmem_free(tmem, kColumns);

@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                             tile_copy4(v_at + c * 2048, &v_map, 64 * c, row, hk, page, bar);
                         }
                     } else {
-                        if (p0 < keys) atomicOr(a.errors, 2u);
+                        if (p0 < keys) atomicOr(a.errors, kErrorInput);
                         barrier_arrive(bar);
                     }
                 }
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                         off = ((((int64_t)page * a.Hkv + hk) << a.page_shift) + (p & ((1 << a.page_shift) - 1))) * D;
                     } else {
                         off = -2;
-                        atomicOr(a.errors, 2u);
+                        atomicOr(a.errors, kErrorInput);
                     }
                 }
                 const int chunk = lane % CH;
@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
     }
     if (!kTiled) copies_wait<0>();
-    if (gave_up_word && tid == 0) atomicOr(a.errors, 4u);
+    if (gave_up_word && tid == 0) atomicOr(a.errors, kErrorWait);
 }
 
 // Joins the pieces of the cut sequences: block x the one that begins in CTA x,
@@ -681,4 +681,15 @@ extern "C" fb_status fb_attn_tree(const void *q, int ldq, int T, int Hq, const f
                                  : launch_tree_rows<__half, 128>(a, *cache, sh, pdl, s));
     return status_of(D == 64 ? launch_tree_rows<__nv_bfloat16, 64>(a, *cache, sh, pdl, s)
                              : launch_tree_rows<__nv_bfloat16, 128>(a, *cache, sh, pdl, s));
+}
+
+extern "C" fb_status fb_attn_errors(unsigned int *flags, int clear) {
+    if (!flags) return FB_ERR_INVALID_VALUE;
+    if (cudaDeviceSynchronize() != cudaSuccess) return FB_ERR_CUDA;
+    void *word = attn_errors_address();
+    if (!word || cudaMemcpy(flags, word, sizeof(unsigned int), cudaMemcpyDeviceToHost) != cudaSuccess)
+        return FB_ERR_CUDA;
+    const unsigned int zero = 0;
+    if (clear && cudaMemcpy(word, &zero, sizeof zero, cudaMemcpyHostToDevice) != cudaSuccess) return FB_ERR_CUDA;
+    return FB_OK;
 }

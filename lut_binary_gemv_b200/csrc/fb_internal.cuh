@@ -59,10 +59,6 @@ inline cudaStream_t as_stream(void *s) { return reinterpret_cast<cudaStream_t>(s
 // SM count of the current device (cached per device).
 int sm_count();
 
-// Device address of the word in which the attention kernels raise their
-// fb_device_errors bits, on the current device (null on a CUDA error).
-void *attn_errors_address();
-
 // Launch through cudaLaunchKernelEx so the launch's own status comes back
 // (no reliance on the thread's last-error slot).  pdl = programmatic
 // dependent launch (the kernel may start before the previous one ends).

@@ -1634,16 +1634,10 @@ extern "C" fb_status fb_gemv_group_scales(const fb_weights *W, int G, const void
 extern "C" fb_status fb_device_errors(unsigned int *flags, int clear) {
     if (!flags) return FB_ERR_INVALID_VALUE;
     if (cudaDeviceSynchronize() != cudaSuccess) return FB_ERR_CUDA;
-    void *words[2] = {nullptr, attn_errors_address()};   // the GEMV kernels' bits and the attention kernels'
-    if (cudaGetSymbolAddress(&words[0], g_error_flags) != cudaSuccess || !words[1]) return FB_ERR_CUDA;
-    unsigned int all = 0;
-    for (void *w : words) {
-        unsigned int bits = 0;
-        if (cudaMemcpy(&bits, w, sizeof bits, cudaMemcpyDeviceToHost) != cudaSuccess) return FB_ERR_CUDA;
-        all |= bits;
-        bits = 0;
-        if (clear && cudaMemcpy(w, &bits, sizeof bits, cudaMemcpyHostToDevice) != cudaSuccess) return FB_ERR_CUDA;
+    if (cudaMemcpyFromSymbol(flags, g_error_flags, sizeof(unsigned int)) != cudaSuccess) return FB_ERR_CUDA;
+    if (clear) {
+        const unsigned int zero = 0;
+        if (cudaMemcpyToSymbol(g_error_flags, &zero, sizeof(unsigned int)) != cudaSuccess) return FB_ERR_CUDA;
     }
-    *flags = all;
     return FB_OK;
 }

@@ -137,6 +137,10 @@ def test_tree_workspace_follows_the_rows(L):
         assert tree(L, **args, ws=FAKE + 4, ws_bytes=size) == WORKSPACE
 
 
+def test_errors_call_refuses_null(L):
+    assert L.fb_attn_errors(None, 0) == INVALID
+
+
 def test_struct_bytes_match_the_structs():
     assert fb._HEADS.size == C.sizeof(fb.FbHeadsStruct) and fb._CACHE.size == C.sizeof(fb.FbKvCacheStruct)
     h = fb.FbHeadsStruct(q=1, k=2, v=3, t=4, T=5, Hq=6, Hkv=7, D=8, ldq=9, ldk=10, ldv=11)

@@ -245,7 +245,7 @@ def test_prompt(case):
     assert (out[cu[-1]:] == 7.5).all() and (lse[cu[-1]:] == -3.25).all()
     again = fb.fb_attn_prompt(q, k, v, cud, scale)
     assert torch.equal(again[:cu[-1]], out[:cu[-1]])                    # deterministic; lse not needed
-    assert fb.fb_device_errors() == 0
+    assert fb.fb_attn_errors() == 0
 
 
 def test_prompt_longer_one_head():
@@ -332,7 +332,7 @@ def test_prompts_on_two_streams_at_once():
             with torch.cuda.stream(s):
                 outs.append(fb.fb_attn_prompt(q, k, v, cud))
     torch.cuda.synchronize()
-    assert all(torch.equal(o, refs[i % 2]) for i, o in enumerate(outs)) and fb.fb_device_errors() == 0
+    assert all(torch.equal(o, refs[i % 2]) for i, o in enumerate(outs)) and fb.fb_attn_errors() == 0
 
 
 def test_prompt_side_stream_and_graph():
@@ -454,7 +454,7 @@ def test_tree(case, chain):
     check_attention(out, lse, tree_refs(c, masks, scale), c["D"], c["dtype"], "tree")
     o2, l2 = tree_call(c, masks, scale, flags=fb.FB_GEMV_PDL)
     assert torch.equal(out, o2) and torch.equal(lse, l2)
-    assert fb.fb_device_errors() == 0
+    assert fb.fb_attn_errors() == 0
 
 
 def test_tree_single_tokens_without_offsets():
@@ -499,13 +499,13 @@ def test_tree_special_values_reach_only_rows_that_see_them(value, Hq, page_size)
 def test_tree_bad_pages_give_nan_and_an_error_bit(where, Hq, page_size):
     c = tree_inputs([300, 20, 45], [2, 1, 1], Hq, 2, 64, page_size, torch.float16, seed=6)
     ref, _ = tree_call(c)
-    assert fb.fb_device_errors() == 0
+    assert fb.fb_attn_errors() == 0
     if where == "width":
         c["table"] = np.ascontiguousarray(c["table"][:, :192 // page_size])   # 192 positions of 302
     else:
         c["table"][0, 3] = c["k"].shape[0] if where == "page" else -7
     out, lse = tree_call(c, None)
-    assert fb.fb_device_errors() == 2 and fb.fb_device_errors() == 0
+    assert fb.fb_attn_errors(clear=False) == 1 and fb.fb_attn_errors() == 1 and fb.fb_attn_errors() == 0
     assert bool(torch.isnan(out[:2]).all()) and bool(torch.isnan(lse[:2]).all())
     assert bool(torch.isfinite(out[2:]).all())
     assert torch.equal(out[2:], ref[2:])
@@ -516,7 +516,7 @@ def test_tree_bad_page_among_the_drafts_reaches_only_rows_that_see_it():
     ref, _ = tree_call(c)
     c["table"][0, 9] = -5                                                 # drafted tokens 8 to 15
     got, lse = tree_call(c)
-    assert fb.fb_device_errors() == 2
+    assert fb.fb_attn_errors() == 1
     for i in range(20):
         if c["masks"][i] >> 8 & 0xFF:
             assert bool(torch.isnan(got[i]).all()) and bool(torch.isnan(lse[i]).all())
@@ -530,11 +530,11 @@ def test_tree_lengths_beyond_every_bound(Hq):
     ref, _ = tree_call(c)
     c["lens"] = [2 ** 31 - 1, 30, -4]
     out, _ = tree_call(c)
-    assert fb.fb_device_errors() == 2
+    assert fb.fb_attn_errors() == 1
     assert bool(torch.isnan(out[0]).all()) and torch.equal(out[1:3], ref[1:3])
     c["lens"] = [100, 30, 0]                                              # a negative length is none
     again, _ = tree_call(c)
-    assert torch.equal(again[3], out[3]) and fb.fb_device_errors() == 0
+    assert torch.equal(again[3], out[3]) and fb.fb_attn_errors() == 0
 
 
 @pytest.mark.parametrize("page_size,Hq,drafts", [(64, 8, 1), (4, 8, 1), (64, 8, 20)])
@@ -558,7 +558,7 @@ def test_tree_and_rope_in_a_cache_past_32_bits(page_size, Hq, drafts):
     lens = torch.tensor([70], dtype=torch.int32, device=DEV)
     out = fb.fb_attn_tree(qr[70:], (k, v), table, lens, cu, drafts)
     want = fb.fb_attn_prompt(qr, kr, vv, torch.tensor([0, T], dtype=torch.int32, device=DEV))[70:]
-    assert fb.fb_device_errors() == 0
+    assert fb.fb_attn_errors() == 0
     assert (out.float() - want.float()).abs().max() <= 4 * HALF[torch.bfloat16] * vv.abs().max()
 
 
@@ -566,10 +566,10 @@ def test_tree_counts_above_max_draft():
     c = tree_inputs([33, 10], [4, 2], 4, 2, 64, 16, torch.float16, seed=7)
     out = torch.full((6, 4, 64), 9.0, dtype=torch.float16, device=DEV)
     ref, _ = tree_call(c, None)
-    fb.fb_device_errors()
+    fb.fb_attn_errors()
     c["drafts"] = [3, 2]                                                  # max_draft = 3
     tree_call(c, None, out=out)
-    assert fb.fb_device_errors() == 2
+    assert fb.fb_attn_errors() == 1
     assert torch.equal(out[:3], ref[:3]) and bool((out[3] == 9.0).all()) and torch.equal(out[4:], ref[4:])
 
 

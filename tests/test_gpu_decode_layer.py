@@ -54,7 +54,7 @@ def test_layer_prompt_then_drafts():
                            torch.tensor(masks, dtype=torch.int64, device=DEV))
     y = fb.fb_gemv_batched(wo, tree.view(n_draft, Hq * D))
     last = fb.fb_gemv(wo, prompt[-1].reshape(-1))
-    assert fb.fb_device_errors() == 0
+    assert fb.fb_attn_errors() == 0
 
     # the same layer in fp64 from the projections on; fp16 queries, keys, values, weights and outputs each round
     # by 2^-11 relative, scores are below 8 * sqrt(8) in size (normed heads), so a weight moves by at most
@@ -117,4 +117,4 @@ def test_decode_step_as_one_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want)
-    assert fb.fb_device_errors() == 0
+    assert fb.fb_attn_errors() == 0

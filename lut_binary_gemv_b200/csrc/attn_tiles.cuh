@@ -649,11 +649,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             }
                     if (kCache && partial && mine) {
                         if constexpr (kCache) {
-                            float4 *part = reinterpret_cast<float4 *>(a.part + ((size_t)it.piece * kBlock + s * kTile + local) * D + c);
+                            // rows side by side, so that a warp writes whole lines
+                            float4 *part = reinterpret_cast<float4 *>(a.part) +
+                                           ((size_t)it.piece * (D / 4) + c / 4) * kBlock + s * kTile + local;
 #pragma unroll
                             for (int i = 0; i < 8; ++i)
-                                part[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                                      __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+                                part[(size_t)i * kBlock] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                                                       __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
                         }
                     } else if (mine) {
 #pragma unroll

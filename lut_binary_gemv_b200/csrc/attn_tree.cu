@@ -520,38 +520,86 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     if (gave_up_word && tid == 0) atomicOr(a.errors, kErrorWait);
 }
 
-// Joins the pieces of the cut sequences: block x the one that begins in CTA x,
-// four rows (eight of 64 elements) a block; the pieces in order.
+// Joins the pieces of the cut items: block x the one that begins in CTA x.  A thread takes four columns of a row;
+// where an item has fewer of them than the block threads, several share its pieces.  Several pieces are asked
+// for before the first is used.  The order is fixed, so results do not depend on timing.
+// The tensor-core tiles leave their rows side by side (a thread a row), the others their columns.
+template <int ROWS>
+constexpr int kJoinThreads = ROWS == kTreeTileRows ? 128 : 512;
+
 template <typename E, int D, int ROWS>
-__global__ void __launch_bounds__(kThreads) join_kernel(const TreeArgs a) {
+__global__ void __launch_bounds__(kJoinThreads<ROWS>) join_kernel(const TreeArgs a) {
+    constexpr bool kRowsBeside = ROWS == kTreeTileRows;
+    constexpr int CH = D / 4, kBlockThreads = kJoinThreads<ROWS>, kAtOnce = kRowsBeside ? 4 : 8;
+    __shared__ float4 s_y[kBlockThreads];
+    __shared__ float2 s_ml[kBlockThreads];
     wait_for_previous_kernel();
     const int4 rec = a.records[blockIdx.x];
     const int row_tiles = rec.w >> 16, rows = rec.w & 0xFFFF;
-    const int row = blockIdx.y * (kThreads * 4 / D) + threadIdx.x / (D / 4), c = threadIdx.x % (D / 4);
-    if (rec.x == 0 || row >= rows) return;
-    const int first = blockIdx.x, last = rec.x - 1;
-    float top = -INFINITY, sum = 0.0f;
-    float4 y = make_float4(0, 0, 0, 0);
-#pragma unroll 4
-    for (int x = first; x <= last; ++x) {
-        const size_t at = (2 * (size_t)x + (x == first ? 1 : 0)) * ROWS + row;
-        const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + at * 2);
-        const float4 v = *reinterpret_cast<const float4 *>(a.part + at * D + 4 * c);
-        const float mn = fmaxf(top, ml.x), ref = mn == -INFINITY ? 0.0f : mn;
-        const float f = exp2_approx(top - ref), g = exp2_approx(ml.x - ref);
-        top = mn;
-        sum = sum * f + ml.y * g;
-        y.x = y.x * f + v.x * g, y.y = y.y * f + v.y * g, y.z = y.z * f + v.z * g, y.w = y.w * f + v.w * g;
+    if (rec.x == 0) return;
+    const int first = blockIdx.x, last = rec.x - 1, tid = threadIdx.x;
+    const int units = kRowsBeside ? ROWS * CH : rows * CH;
+    // threads that share a unit: as many as fit, a power of two, no more than there are pieces
+    int shares = 1;
+    while (!kRowsBeside && 2 * shares * units <= kBlockThreads && 2 * shares <= last - first + 1) shares *= 2;
+    const int at_once = shares > 1 ? units : kBlockThreads;   // units a pass
+    for (int u0 = blockIdx.y * at_once; u0 < units; u0 += gridDim.y * at_once) {
+        const int unit = u0 + tid % at_once, share = tid / at_once;
+        const int row = kRowsBeside ? unit % ROWS : unit / CH, c = kRowsBeside ? unit / ROWS : unit % CH;
+        const bool mine = unit < units && row < rows && share < shares;
+        float top = -INFINITY, sum = 0.0f;
+        float4 y = make_float4(0, 0, 0, 0);
+        for (int x0 = first + share; mine && x0 <= last; x0 += kAtOnce * shares) {
+            float2 ml[kAtOnce];
+            float4 v[kAtOnce];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                const int x = x0 + i * shares;
+                ml[i] = make_float2(-INFINITY, 0.0f), v[i] = make_float4(0, 0, 0, 0);
+                if (x > last) continue;
+                const size_t piece = 2 * (size_t)x + (x == first ? 1 : 0);
+                ml[i] = *reinterpret_cast<const float2 *>(a.part_ml + (piece * ROWS + row) * 2);
+                v[i] = reinterpret_cast<const float4 *>(a.part)[kRowsBeside ? (piece * CH + c) * ROWS + row : (piece * ROWS + row) * CH + c];
+            }
+            float best = top;
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) best = fmaxf(best, ml[i].x);
+            const float ref = best == -INFINITY ? 0.0f : best, f = exp2_approx(top - ref);
+            top = best, sum *= f, y.x *= f, y.y *= f, y.z *= f, y.w *= f;
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                const float g = exp2_approx(ml[i].x - ref);
+                sum = fmaf(g, ml[i].y, sum);
+                y.x = fmaf(g, v[i].x, y.x), y.y = fmaf(g, v[i].y, y.y), y.z = fmaf(g, v[i].z, y.z), y.w = fmaf(g, v[i].w, y.w);
+            }
+        }
+        if (shares > 1) {   // one pass: the block's threads meet once
+            s_ml[tid] = make_float2(top, sum), s_y[tid] = y;
+            __syncthreads();
+            if (share == 0) {
+                float best = -INFINITY;
+                for (int i = 0; i < shares; ++i) best = fmaxf(best, s_ml[tid + i * units].x);
+                const float ref = best == -INFINITY ? 0.0f : best;
+                top = best, sum = 0.0f, y = make_float4(0, 0, 0, 0);
+                for (int i = 0; i < shares; ++i) {
+                    const float g = exp2_approx(s_ml[tid + i * units].x - ref);
+                    const float4 v = s_y[tid + i * units];
+                    sum = fmaf(g, s_ml[tid + i * units].y, sum);
+                    y.x = fmaf(g, v.x, y.x), y.y = fmaf(g, v.y, y.y), y.z = fmaf(g, v.z, y.z), y.w = fmaf(g, v.w, y.w);
+                }
+            }
+        }
+        if (!mine || share > 0) continue;
+        const int hk = rec.z / row_tiles, rr = rec.z % row_tiles * ROWS + row;
+        const int token = rec.y + rr / a.group, h = hk * a.group + rr % a.group;
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        uint2 packed;
+        packed.x = pack2<E>(y.x * inv, y.y * inv), packed.y = pack2<E>(y.z * inv, y.w * inv);
+        *reinterpret_cast<uint2 *>((E *)a.out + (size_t)token * a.ldo + (size_t)h * D + 4 * c) = packed;
+        if (a.lse && c == 0)
+            a.lse[(size_t)token * a.Hkv * a.group + h] =
+                sum == 0.0f ? -INFINITY : ((top == -INFINITY ? 0.0f : top) + log2f(sum)) * 0.69314718056f;
     }
-    const int hk = rec.z / row_tiles, rr = rec.z % row_tiles * ROWS + row;
-    const int token = rec.y + rr / a.group, h = hk * a.group + rr % a.group;
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    uint2 packed;
-    packed.x = pack2<E>(y.x * inv, y.y * inv), packed.y = pack2<E>(y.z * inv, y.w * inv);
-    *reinterpret_cast<uint2 *>((E *)a.out + (size_t)token * a.ldo + (size_t)h * D + 4 * c) = packed;
-    if (a.lse && c == 0)
-        a.lse[(size_t)token * a.Hkv * a.group + h] =
-            sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718056f;
 }
 
 // The rows of a piece, and its CTAs: by the rows that a key head has at most.
@@ -579,7 +627,8 @@ Workspace workspace(const Shape &sh, int D) {
 
 template <typename E, int D, int ROWS>
 cudaError_t launch_join(const TreeArgs &a, int ctas, cudaStream_t s) {
-    return launch(join_kernel<E, D, ROWS>, dim3(ctas, ROWS * D / 4 / kThreads), dim3(kThreads), 0, s, true, a);
+    const int passes = ROWS == kTreeTileRows ? ROWS * D / 4 / kJoinThreads<ROWS> : 1;
+    return launch(join_kernel<E, D, ROWS>, dim3(ctas, passes), dim3(kJoinThreads<ROWS>), 0, s, true, a);
 }
 
 template <typename E, int D, int WR, int WK, int MT, bool kTiled>

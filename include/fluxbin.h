@@ -394,8 +394,10 @@ FB_API fb_status fb_attn_prompt(const fb_heads *in, const int32_t *cu_seqlens, i
  * results of sequences split over several CTAs; its contents need not be
  * set up and mean nothing afterwards, but calls that may run at the same
  * time (on several streams, in several captured graphs) need one each.
- * fb_attn_tree_workspace_bytes is host only; 0 for invalid sizes. */
-FB_API size_t fb_attn_tree_workspace_bytes(int Hq, int Hkv, int D, int max_draft);
+ * fb_attn_tree_workspace_bytes is host only; 0 where the call needs none
+ * (tables of at most 512 keys are not split; ws may be NULL) and for invalid
+ * sizes. */
+FB_API size_t fb_attn_tree_workspace_bytes(int Hq, const fb_kv_cache *cache, int max_draft, int table_width);
 FB_API fb_status fb_attn_tree(const void *q, int ldq, int T, int Hq, const fb_kv_cache *cache,
                               const int32_t *page_table, int table_width, int ld_table, const int32_t *lens,
                               const int32_t *cu_draft, int n, int max_draft, const uint64_t *mask, float scale, void *out, int ldo, float *lse,

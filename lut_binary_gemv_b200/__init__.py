@@ -109,7 +109,7 @@ def lib() -> C.CDLL:
             "fb_fit_base": (I, [P, I, I, I, I, P, I, P, P, P]),
             "fb_qk_norm_rope": (I, [H, H, P, P, I, P, P, F, KV, P, U, P]),
             "fb_attn_prompt": (I, [H, P, I, F, P, I, P, U, P]),
-            "fb_attn_tree_workspace_bytes": (S, [I, I, I, I]),
+            "fb_attn_tree_workspace_bytes": (S, [I, KV, I, I]),
             "fb_attn_errors": (I, [P, I]),
             "fb_attn_tree": (I, [P, I, I, I, KV, P, I, I, P, P, I, I, P, F, P, I, P, P, S, U, P]),
             "fb_status_string": (C.c_char_p, [I]),
@@ -449,42 +449,45 @@ def _on(device: int, f, *args) -> int:
     return f(*args, torch.cuda.current_stream(device).cuda_stream if _raw_stream is None else _raw_stream(device))
 
 
-def _head_rows(t: torch.Tensor, what: str, device: int, shape, dtype) -> int:
+def _rows(t: torch.Tensor, what: str, device: int, shape, dtype) -> int:
     """The row pitch of [T, H, D] heads on the GPU whose heads are contiguous within a row."""
-    st = t.stride()
-    if t.shape != shape or t.dtype != dtype or t.get_device() != device or device < 0:
-        raise ValueError(f"{what}: a {dtype} tensor {tuple(shape)} on the GPU of the others is expected, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    T, H, D = shape
-    if (st[2] != 1 and D > 1) or (st[1] != D and H > 1):
+    if t.dtype == dtype and t.shape == shape and t.get_device() == device >= 0:
+        T, H, D = shape
+        if t.is_contiguous():
+            return H * D
+        st = t.stride()
+        if (st[2] == 1 or D == 1) and (st[1] == D or H == 1):
+            return st[0] if T > 1 else H * D
         raise ValueError(f"{what}: the heads of a row must be contiguous (only rows may be strided)")
-    return st[0] if T > 1 else H * D
+    raise ValueError(f"{what}: a {dtype} tensor {tuple(shape)} on the GPU of the others is expected, "
+                     f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def _sizes(q: torch.Tensor, k: torch.Tensor):
-    if q.dim() != 3 or k.dim() != 3 or q.dtype not in _DTYPES:
+    """The shape of the queries, of the keys and values, and their type's code."""
+    qs, ks = q.shape, k.shape
+    t = _DTYPES.get(q.dtype)
+    if len(qs) != 3 or len(ks) != 3 or t is None:
         raise ValueError("q, k, v: [T, heads, D] tensors (f32/f16/bf16)")
-    return q.shape, k.shape
+    return qs, (qs[0], ks[1], qs[2]), t
 
 
-def _flat(t: Optional[torch.Tensor], what: str, dtype, n: int, device: int) -> Optional[int]:
-    """The address of a contiguous tensor of n elements of the given type (None passes)."""
-    if t is None:
-        return None
-    if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != device:
+def _flat(t: torch.Tensor, what: str, dtype, n: int, device: int) -> int:
+    """The address of a contiguous tensor of n elements of the given type."""
+    if t.dtype != dtype or t.numel() != n or t.get_device() != device or not t.is_contiguous():
         raise ValueError(f"{what}: a contiguous {dtype} tensor of {n} elements on the GPU of the others is expected")
     return t.data_ptr()
 
 
 def _cache_bytes(cache, device: int, dtype):
-    """(k_pages, v_pages), each [pages, Hkv, page_size, D] -> the C struct and its sizes."""
+    """(k_pages, v_pages), each [pages, Hkv, page_size, D] -> the C struct and the shape."""
     k, v = cache
     shape = k.shape
-    if (len(shape) != 4 or v.shape != shape or k.dtype != dtype or v.dtype != dtype or not k.is_contiguous()
-            or not v.is_contiguous() or k.get_device() != device or v.get_device() != device):
+    if (len(shape) != 4 or v.shape != shape or k.dtype != dtype or v.dtype != dtype or k.get_device() != device
+            or v.get_device() != device or not k.is_contiguous() or not v.is_contiguous()):
         raise ValueError("cache: two contiguous [pages, Hkv, page_size, D] tensors of the heads' type and device")
     pages, Hkv, page_size, D = shape
-    return _CACHE.pack(k.data_ptr(), v.data_ptr(), _DTYPES[dtype], pages, page_size, Hkv, D), Hkv, D
+    return _CACHE.pack(k.data_ptr(), v.data_ptr(), _DTYPES[dtype], pages, page_size, Hkv, D), shape
 
 
 def rope_frequencies(rot: int, theta: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -507,16 +510,17 @@ def fb_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: Opti
     Returns (q_out, k_out, v_out): q_out is made when not given; k_out and v_out are made only where there is no
     cache.  Their type is out_dtype: by default the cache's, else a given output's, else the heads' (bf16 for
     f32 heads).  The outputs may be the inputs (in place)."""
-    qs, ks = _sizes(q, k)
+    qs, ks, t = _sizes(q, k)
     T, Hq, D = qs
-    Hkv, dev, t = ks[1], q.get_device(), q.dtype
-    ks = (T, Hkv, D)
-    ldq, ldk, ldv = _head_rows(q, "q", dev, qs, t), _head_rows(k, "k", dev, ks, t), _head_rows(v, "v", dev, ks, t)
+    Hkv, dev, dtype = ks[1], q.get_device(), q.dtype
+    hin = _HEADS.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), t, T, Hq, Hkv, D, _rows(q, "q", dev, qs, dtype),
+                      _rows(k, "k", dev, ks, dtype), _rows(v, "v", dev, ks, dtype))
     dt = out_dtype
     if dt is None:
         given = cache[0] if cache is not None else next((o for o in (q_out, k_out, v_out) if o is not None), None)
-        dt = given.dtype if given is not None else t if t != torch.float32 else torch.bfloat16
-    if dt not in _DTYPES:
+        dt = given.dtype if given is not None else dtype if t else torch.bfloat16
+    to = _DTYPES.get(dt)
+    if to is None:
         raise ValueError("out_dtype: torch.float16 or torch.bfloat16")
     if q_out is None:
         q_out = torch.empty(qs, dtype=dt, device=q.device)
@@ -526,21 +530,22 @@ def fb_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: Opti
         v_out = torch.empty(ks, dtype=dt, device=q.device) if v_out is None else v_out
     else:
         kv = _cache_bytes(cache, dev, dt)[0]
+    kp = vp = ldk = ldv = 0
+    if k_out is not None:
+        kp, ldk = k_out.data_ptr(), _rows(k_out, "k_out", dev, ks, dt)
+    if v_out is not None:
+        vp, ldv = v_out.data_ptr(), _rows(v_out, "v_out", dev, ks, dt)
     rot = 0 if inv_freq is None else 2 * inv_freq.numel()
     if rot and pos is None:
         raise ValueError("pos: int32 [T] where there is a rotation")
     if (cache is None) != (slots is None):
         raise ValueError("cache and slots go together")
-    hin = _HEADS.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), _DTYPES[t], T, Hq, Hkv, D, ldq, ldk, ldv)
-    hout = _HEADS.pack(q_out.data_ptr(), 0 if k_out is None else k_out.data_ptr(),
-                       0 if v_out is None else v_out.data_ptr(), _DTYPES[dt], T, Hq, Hkv, D,
-                       _head_rows(q_out, "q_out", dev, qs, dt),
-                       0 if k_out is None else _head_rows(k_out, "k_out", dev, ks, dt),
-                       0 if v_out is None else _head_rows(v_out, "v_out", dev, ks, dt))
-    _check(_on(dev, lib().fb_qk_norm_rope, hin, hout, _flat(pos, "pos", torch.int32, T, dev),
-               _flat(inv_freq, "inv_freq", torch.float64, rot // 2, dev), rot,
-               _flat(q_weight, "q_weight", torch.float32, D, dev), _flat(k_weight, "k_weight", torch.float32, D, dev),
-               eps, kv, _flat(slots, "slots", torch.int32, T, dev),
+    hout = _HEADS.pack(q_out.data_ptr(), kp, vp, to, T, Hq, Hkv, D, _rows(q_out, "q_out", dev, qs, dt), ldk, ldv)
+    _check(_on(dev, lib().fb_qk_norm_rope, hin, hout, None if pos is None else _flat(pos, "pos", torch.int32, T, dev),
+               _flat(inv_freq, "inv_freq", torch.float64, rot // 2, dev) if rot else None, rot,
+               None if q_weight is None else _flat(q_weight, "q_weight", torch.float32, D, dev),
+               None if k_weight is None else _flat(k_weight, "k_weight", torch.float32, D, dev), eps, kv,
+               None if slots is None else _flat(slots, "slots", torch.int32, T, dev),
                flags | FB_ROPE_NEIGHBOURS if interleaved else flags), "fb_qk_norm_rope")
     return q_out, k_out, v_out
 
@@ -552,23 +557,24 @@ def fb_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens
     strided), sequence s being tokens cu_seqlens[s] .. cu_seqlens[s+1]-1 (int32 [n+1]) -> [T, Hq, D].  scale
     defaults to D^-0.5; lse float32 [T, Hq] takes the logarithms of the softmax's sums.  Rows of no sequence keep
     what `out` holds (unset memory when it is not given)."""
-    qs, ks = _sizes(q, k)
+    qs, ks, t = _sizes(q, k)
     T, Hq, D = qs
-    Hkv, dev, t = ks[1], q.get_device(), q.dtype
-    ks = (T, Hkv, D)
-    h = _HEADS.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), _DTYPES[t], T, Hq, Hkv, D,
-                    _head_rows(q, "q", dev, qs, t), _head_rows(k, "k", dev, ks, t), _head_rows(v, "v", dev, ks, t))
+    dev, dtype = q.get_device(), q.dtype
+    h = _HEADS.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), t, T, Hq, ks[1], D, _rows(q, "q", dev, qs, dtype),
+                    _rows(k, "k", dev, ks, dtype), _rows(v, "v", dev, ks, dtype))
     if out is None:
-        out = torch.empty(qs, dtype=t, device=q.device)
+        out = torch.empty(qs, dtype=dtype, device=q.device)
     n = cu_seqlens.numel() - 1
     _check(_on(dev, lib().fb_attn_prompt, h, _flat(cu_seqlens, "cu_seqlens", torch.int32, n + 1, dev), n,
-               D ** -0.5 if scale is None else scale, out.data_ptr(), _head_rows(out, "out", dev, qs, t),
-               _flat(lse, "lse", torch.float32, T * Hq, dev), flags), "fb_attn_prompt")
+               D ** -0.5 if scale is None else scale, out.data_ptr(), _rows(out, "out", dev, qs, dtype),
+               None if lse is None else _flat(lse, "lse", torch.float32, T * Hq, dev), flags), "fb_attn_prompt")
     return out
 
 
-def fb_attn_tree_workspace_bytes(Hq: int, Hkv: int, D: int, max_draft: int = 1) -> int:
-    return lib().fb_attn_tree_workspace_bytes(Hq, Hkv, D, max_draft)
+def fb_attn_tree_workspace_bytes(Hq: int, cache, max_draft: int, table_width: int) -> int:
+    """Bytes of the workspace that fb_attn_tree needs (0: none) for Hq query heads over the cache."""
+    return lib().fb_attn_tree_workspace_bytes(Hq, _cache_bytes(cache, cache[0].get_device(), cache[0].dtype)[0],
+                                              max_draft, table_width)
 
 
 def fb_attn_tree(q: torch.Tensor, cache, page_table: torch.Tensor, lens: torch.Tensor,
@@ -582,32 +588,42 @@ def fb_attn_tree(q: torch.Tensor, cache, page_table: torch.Tensor, lens: torch.T
     cache at positions lens[s] + j.  mask int64 [T]: bit j of a token's word lets it see drafted token j of its
     sequence (None: a chain, j <= i).  Returns [T, Hq, D]; scale, out and lse as for fb_attn_prompt.  ws (uint8)
     is made when not given."""
-    if q.dim() != 3:
+    qs, dtype, dev = q.shape, q.dtype, q.get_device()
+    if len(qs) != 3 or dtype not in _DTYPES:
         raise ValueError("q: a [T, heads, D] tensor of the cache's type")
-    qs, t, dev = q.shape, q.dtype, q.get_device()
     T, Hq, D = qs
-    ldq = _head_rows(q, "q", dev, qs, t)
-    kv, Hkv, width = _cache_bytes(cache, dev, t)
-    if width != D:
+    ldq = _rows(q, "q", dev, qs, dtype)
+    kv, shape = _cache_bytes(cache, dev, dtype)
+    if shape[3] != D:
         raise ValueError("cache: another head width than q's")
-    n = lens.numel()
-    ts = page_table.shape
-    if len(ts) != 2 or ts[0] != n or page_table.dtype != torch.int32 or page_table.get_device() != dev or (
-            page_table.stride(1) != 1 and ts[1] > 1):
-        raise ValueError("page_table: an int32 [n, width] tensor with unit column stride on q's device")
+    n, ts = lens.numel(), page_table.shape
+    if len(ts) != 2 or ts[0] != n or page_table.dtype != torch.int32 or page_table.get_device() != dev:
+        raise ValueError("page_table: an int32 [n, width] tensor on q's device")
+    width = ld = ts[1]
+    if not page_table.is_contiguous():
+        ld, unit = page_table.stride()
+        if (unit != 1 and width > 1) or (ld < width and n > 1):
+            raise ValueError("page_table: unit column stride")
+        ld = ld if n > 1 else width
     if out is None:
-        out = torch.empty(qs, dtype=t, device=q.device)
+        out = torch.empty(qs, dtype=dtype, device=q.device)
     if ws is None:
-        ws = torch.empty(max(lib().fb_attn_tree_workspace_bytes(Hq, Hkv, D, max_draft), 16), dtype=torch.uint8,
-                         device=q.device)
+        wb = lib().fb_attn_tree_workspace_bytes(Hq, kv, max_draft, width)
+        wp = None
+        if wb:
+            ws = torch.empty(wb, dtype=torch.uint8, device=q.device)
+            wp = ws.data_ptr()
     elif ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError("ws: a contiguous tensor on q's device")
-    _check(_on(dev, lib().fb_attn_tree, q.data_ptr(), ldq, T, Hq, kv, page_table.data_ptr(), ts[1],
-               page_table.stride(0) if n > 1 else ts[1], _flat(lens, "lens", torch.int32, n, dev),
-               _flat(cu_draft, "cu_draft", torch.int32, n + 1, dev), n, max_draft,
-               _flat(mask, "mask", torch.int64, T, dev), D ** -0.5 if scale is None else scale, out.data_ptr(),
-               _head_rows(out, "out", dev, qs, t), _flat(lse, "lse", torch.float32, T * Hq, dev), ws.data_ptr(),
-               ws.numel() * ws.element_size(), flags), "fb_attn_tree")
+    else:
+        wp, wb = ws.data_ptr(), ws.numel() * ws.element_size()
+    _check(_on(dev, lib().fb_attn_tree, q.data_ptr(), ldq, T, Hq, kv, page_table.data_ptr(), width, ld,
+               _flat(lens, "lens", torch.int32, n, dev),
+               None if cu_draft is None else _flat(cu_draft, "cu_draft", torch.int32, n + 1, dev), n, max_draft,
+               None if mask is None else _flat(mask, "mask", torch.int64, T, dev),
+               D ** -0.5 if scale is None else scale, out.data_ptr(), _rows(out, "out", dev, qs, dtype),
+               None if lse is None else _flat(lse, "lse", torch.float32, T * Hq, dev), wp, wb, flags),
+           "fb_attn_tree")
     return out
 
 

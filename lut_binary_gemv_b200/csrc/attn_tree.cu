@@ -602,14 +602,17 @@ __global__ void __launch_bounds__(kJoinThreads<ROWS>) join_kernel(const TreeArgs
     }
 }
 
-// The rows of a piece, and its CTAs: by the rows that a key head has at most.
+// How a call is cut: the rows of a piece, by the rows that a key head has at most, and the CTAs.
 struct Shape {
     int rows, ctas;
     bool tiles;   // on the fifth-generation tensor cores
+    bool whole;   // items are not cut: where every sequence is short, that gains less than the second launch costs
 };
-Shape shape_of(int most_rows, int group, int page_size) {
-    if (most_rows > 32 && 128 % group == 0 && page_size >= 8) return {kTreeTileRows, sm_count(), true};
-    return {most_rows <= 16 ? 16 : most_rows <= 32 ? 32 : 64, sm_count() * kCtasPerSm, false};
+Shape shape_of(int Hq, const fb_kv_cache &c, int max_draft, int table_width) {
+    const int group = Hq / c.Hkv, most = max_draft * group;
+    if (most > 32 && 128 % group == 0 && c.page_size >= 8) return {kTreeTileRows, sm_count(), true, false};
+    return {most <= 16 ? 16 : most <= 32 ? 32 : 64, sm_count() * kCtasPerSm, false,
+            (int64_t)table_width * c.page_size <= kWholeKeys};
 }
 
 // The workspace: the pieces' outputs, their maxima and sums, a record a CTA.
@@ -680,13 +683,12 @@ void *attn_errors_address() {
 
 using namespace fb;
 
-extern "C" size_t fb_attn_tree_workspace_bytes(int Hq, int Hkv, int D, int max_draft) {
-    if (Hq < 1 || Hq > kMaxHeads || Hkv < 1 || Hq % Hkv || (D != 64 && D != 128) || max_draft < 1 || max_draft > 64)
+extern "C" size_t fb_attn_tree_workspace_bytes(int Hq, const fb_kv_cache *cache, int max_draft, int table_width) {
+    if (!cache || !valid_cache(*cache) || Hq < 1 || Hq > kMaxHeads || Hq % cache->Hkv ||
+        (cache->D != 64 && cache->D != 128) || max_draft < 1 || max_draft > 64 || table_width < 1)
         return 0;
-    // either shape, whatever the page size
-    const int group = Hq / Hkv, rows = max_draft * group;
-    const size_t a = workspace(shape_of(rows, group, 1), D).bytes, b = workspace(shape_of(rows, group, 8), D).bytes;
-    return a > b ? a : b;
+    const Shape sh = shape_of(Hq, *cache, max_draft, table_width);
+    return sh.whole ? 0 : workspace(sh, cache->D).bytes;
 }
 
 extern "C" fb_status fb_attn_tree(const void *q, int ldq, int T, int Hq, const fb_kv_cache *cache,
@@ -706,23 +708,22 @@ extern "C" fb_status fb_attn_tree(const void *q, int ldq, int T, int Hq, const f
         ldo % 8 || !aligned(page_table, 4) || !aligned(lens, 4) || !aligned(cu_draft, 4) || !aligned(mask, 8) ||
         !aligned(lse, 4))
         return FB_ERR_MISALIGNED;
-    if (!ws || !aligned(ws, 16) || ws_bytes < fb_attn_tree_workspace_bytes(Hq, cache->Hkv, D, max_draft))
-        return FB_ERR_WORKSPACE;
     const int group = Hq / cache->Hkv;
-    const Shape sh = shape_of(max_draft * group, group, cache->page_size);
+    const Shape sh = shape_of(Hq, *cache, max_draft, table_width);
     const Workspace w = workspace(sh, D);
+    if (!sh.whole && (!ws || !aligned(ws, 16) || ws_bytes < w.bytes)) return FB_ERR_WORKSPACE;
     TreeArgs a = {};
     a.q = q, a.kc = cache->k, a.vc = cache->v, a.out = out, a.lse = lse;
     a.table = page_table, a.lens = lens, a.cu = cu_draft, a.mask = mask;
-    a.part = (float *)ws, a.part_ml = (float *)((char *)ws + w.ml), a.records = (int4 *)((char *)ws + w.records);
+    if (!sh.whole)
+        a.part = (float *)ws, a.part_ml = (float *)((char *)ws + w.ml), a.records = (int4 *)((char *)ws + w.records);
     a.n = n, a.T = T, a.Hkv = cache->Hkv, a.group = group, a.ldq = ldq, a.ldo = ldo;
     a.table_width = table_width, a.ld_table = ld_table, a.max_draft = max_draft;
     a.pages = cache->pages, a.page_shift = log2_of(cache->page_size);
     a.scale_log2 = scale * 1.44269504089f;
     a.errors = (unsigned int *)attn_errors_address();
     if (!a.errors) return FB_ERR_CUDA;
-    // Where every sequence is short, cutting gains less than the second launch costs.
-    a.whole = !sh.tiles && (int64_t)table_width * cache->page_size <= kWholeKeys;
+    a.whole = sh.whole;
     const bool pdl = flags & FB_GEMV_PDL;
     cudaStream_t s = as_stream(stream);
     if (cache->t == FB_F16)

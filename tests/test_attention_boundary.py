@@ -93,7 +93,7 @@ def test_prompt_refusals(L, args, status):
     assert prompt(L, **args) == status
 
 
-def tree(L, q=FAKE, ldq=1024, T=4, Hq=8, cache=None, table=FAKE, width=8, ld=8, lens=FAKE, cu=FAKE, n=2, most=3,
+def tree(L, q=FAKE, ldq=1024, T=4, Hq=8, cache=None, table=FAKE, width=80, ld=80, lens=FAKE, cu=FAKE, n=2, most=3,
          mask=FAKE, scale=0.1, out=OUT, ldo=1024, lse=FAKE, ws=FAKE, ws_bytes=1 << 30, flags=0):
     kv = cache or kv_cache()
     return L.fb_attn_tree(q, ldq, T, Hq, C.byref(kv), table, width, ld, lens, cu, n, most, mask, scale, out, ldo, lse,
@@ -104,7 +104,7 @@ def tree(L, q=FAKE, ldq=1024, T=4, Hq=8, cache=None, table=FAKE, width=8, ld=8, 
     (dict(q=None), INVALID), (dict(table=None), INVALID), (dict(lens=None), INVALID), (dict(out=None), INVALID),
     (dict(T=0), INVALID), (dict(Hq=7), INVALID), (dict(Hq=0), INVALID), (dict(n=0), INVALID), (dict(n=65537), INVALID),
     (dict(cu=None), INVALID), (dict(most=0), INVALID), (dict(most=65), INVALID), (dict(width=0), INVALID),
-    (dict(ld=7), INVALID), (dict(ldq=1016), INVALID), (dict(ldo=8), INVALID), (dict(scale=0.0), INVALID),
+    (dict(ld=79), INVALID), (dict(ldq=1016), INVALID), (dict(ldo=8), INVALID), (dict(scale=0.0), INVALID),
     (dict(scale=math.nan), INVALID), (dict(flags=2), INVALID), (dict(cache=kv_cache(t=F32)), INVALID),
     (dict(cache=kv_cache(page_size=0)), INVALID), (dict(cache=kv_cache(v=None)), INVALID),
     (dict(cache=kv_cache(D=96), ldq=1024), UNSUPPORTED),
@@ -119,22 +119,29 @@ def test_tree_refusals(L, args, status):
 
 
 def test_tree_workspace_bytes(L):
-    assert L.fb_attn_tree_workspace_bytes(64, 8, 128, 1) > 0
-    for bad in [(0, 1, 128, 1), (8, 3, 128, 1), (8, 0, 128, 1), (8, 8, 96, 1), (8, 8, 64, 0), (8, 8, 64, 65),
-                (2048, 8, 64, 1)]:
-        assert L.fb_attn_tree_workspace_bytes(*bad) == 0
+    def size(Hq=64, most=1, width=100, **over):
+        c = kv_cache(**{**dict(Hkv=8, page_size=64), **over})
+        return L.fb_attn_tree_workspace_bytes(Hq, C.byref(c), most, width)
+    sizes = [size(most=m) for m in (1, 2, 4, 5, 64)]
+    assert 0 < sizes[0] == sizes[1] < sizes[2] < sizes[3] == sizes[4]    # up to 16, 32 and more rows a key head
+    assert size(D=64) < sizes[0]
+    assert size(most=64, page_size=4) < sizes[4]                         # small pages: 64 rows at a time
+    assert size(width=8) == size(page_size=1, width=512) == 0 < size(width=9)   # short tables are not split
+    assert size(most=64, width=8) == sizes[4]
+    for bad in (dict(Hq=0), dict(Hq=2048), dict(Hq=63), dict(most=0), dict(most=65), dict(width=0), dict(D=96),
+                dict(page_size=3), dict(k=None), dict(t=F32)):
+        assert size(**bad) == 0
+    assert L.fb_attn_tree_workspace_bytes(8, None, 1, 1) == 0
 
 
-def test_tree_workspace_follows_the_rows(L):
-    sizes = [L.fb_attn_tree_workspace_bytes(64, 8, 128, m) for m in (1, 2, 4, 5, 64)]
-    assert sizes[0] == sizes[1] < sizes[2] < sizes[3] == sizes[4]        # up to 16, 32 and more rows a key head
-    assert L.fb_attn_tree_workspace_bytes(64, 8, 64, 1) < sizes[0]
-    # a workspace one byte short is refused, whatever the page size
-    for size, page in ((sizes[4], 16), (sizes[4], 64)):
+def test_tree_refuses_a_workspace_that_is_too_small(L):
+    for page, most in ((16, 1), (16, 64), (4, 64)):
         c = kv_cache(Hkv=8, page_size=page)
-        args = dict(q=FAKE, ldq=8192, T=64, Hq=64, cache=c, n=2, most=64, ldo=8192)
-        assert tree(L, **args, ws_bytes=0) == WORKSPACE
+        size = L.fb_attn_tree_workspace_bytes(64, C.byref(c), most, 1000)
+        args = dict(q=FAKE, ldq=8192, T=64, Hq=64, cache=c, width=1000, ld=1000, n=2, most=most, ldo=8192)
+        assert tree(L, **args, ws_bytes=size - 1) == WORKSPACE
         assert tree(L, **args, ws=FAKE + 4, ws_bytes=size) == WORKSPACE
+        assert tree(L, **args, ws=None, ws_bytes=size) == WORKSPACE
 
 
 def test_errors_call_refuses_null(L):

@@ -600,7 +600,7 @@ def test_tree_graphs_with_a_workspace_each(drafts):
     table, lens = torch.tensor(c["table"], device=DEV), torch.tensor(c["lens"], dtype=torch.int32, device=DEV)
     ref = fb.fb_attn_tree(c["q"], (c["k"], c["v"]), table, lens, cu, drafts)
     outs = [torch.empty_like(ref) for _ in range(2)]
-    wss = [torch.full((fb.fb_attn_tree_workspace_bytes(16, 2, 128, drafts),), 255, dtype=torch.uint8, device=DEV)
+    wss = [torch.full((fb.fb_attn_tree_workspace_bytes(16, (c["k"], c["v"]), drafts, table.shape[1]),), 255, dtype=torch.uint8, device=DEV)
            for _ in range(2)]
     graphs = []
     for o, w in zip(outs, wss):

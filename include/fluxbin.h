@@ -386,10 +386,10 @@ FB_API fb_status fb_attn_prompt(const fb_heads *in, const int32_t *cu_seqlens, i
  * among the keys that a row sees gives NaN in that row, and a sequence of
  * more than max_draft tokens leaves those behind them unwritten; both raise
  * bit 0 of fb_attn_errors, and no memory outside the cache is read.  Tokens
- * of no sequence keep their contents.  Where a key head has more than 32 rows
- * (max_draft * Hq / Hkv), Hq / Hkv divides 128 and page_size >= 8, the weights
- * are rounded as in fb_attn_prompt; otherwise they keep 2^-16 of their size,
- * and an infinite value among the committed keys gives infinity or NaN.
+ * of no sequence keep their contents.  Where a key head has at most 16 rows
+ * (max_draft * Hq / Hkv) the weights keep 2^-16 of their size, and an infinite
+ * value among the committed keys gives infinity or NaN; with more rows they
+ * are rounded as in fb_attn_prompt.
  * ws: fb_attn_tree_workspace_bytes bytes, 16-byte aligned, for the partial
  * results of sequences split over several CTAs; its contents need not be
  * set up and mean nothing afterwards, but calls that may run at the same

@@ -122,6 +122,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     constexpr int kHalf = kSlice<D> / 2;    // from a slice's keys to its values
     constexpr bool kOwnKeys = WK == kWarps; // a warp multiplies the keys it loads, and no others
     constexpr bool kQueriesHeld = MT == 1;  // the queries stay in registers
+    constexpr bool kTwoParts = MT == 1;     // the weights as two operands
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ __align__(8) uint64_t full[S][kWarps];
     __shared__ uint64_t s_mask[ROWS];
@@ -355,9 +356,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                         for (int j = 0; j < D / 8; ++j) o[t][j][2 * half] *= f, o[t][j][2 * half + 1] *= f;
                     }
             }
-            // The weights meet the values as two operands, the rounded weight and what the rounding left: beside the
-            // stream of keys the second product costs nothing for up to 16 rows and 3% for up to 32, and the weights
-            // lose no more than 2^-16 of their size.
+            // For up to 16 rows the weights meet the values as two operands, the rounded weight and what the rounding
+            // left: beside the stream of keys the second product costs nothing there, and the weights lose no more
+            // than 2^-16 of their size.  For more rows it would cost 12%; there they are rounded once.
             uint32_t pa[MT][NT / 2][4], pr[MT][NT / 2][4];
 #pragma unroll
             for (int t = 0; t < MT; ++t)
@@ -372,8 +373,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                         sum += p0 + p1;
                         const uint32_t near = pack2<E>(p0, p1);
                         pa[t][j / 2][(j % 2) * 2 + half] = near;
-                        const float2 had = unpack2<E>(near);
-                        pr[t][j / 2][(j % 2) * 2 + half] = pack2<E>(p0 - had.x, p1 - had.y);
+                        if constexpr (kTwoParts) {
+                            const float2 had = unpack2<E>(near);
+                            pr[t][j / 2][(j % 2) * 2 + half] = pack2<E>(p0 - had.x, p1 - had.y);
+                        }
                     }
                     l[t][half] += sum;
                 }
@@ -440,7 +443,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
                     for (int t = 0; t < MT; ++t) {
                         mma<E>(o[t][2 * d], pa[t][c], vb[0], vb[1]), mma<E>(o[t][2 * d + 1], pa[t][c], vb[2], vb[3]);
-                        mma<E>(o[t][2 * d], pr[t][c], vb[0], vb[1]), mma<E>(o[t][2 * d + 1], pr[t][c], vb[2], vb[3]);
+                        if constexpr (kTwoParts)
+                            mma<E>(o[t][2 * d], pr[t][c], vb[0], vb[1]), mma<E>(o[t][2 * d + 1], pr[t][c], vb[2], vb[3]);
                     }
                 }
 

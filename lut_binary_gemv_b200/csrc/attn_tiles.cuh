@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     l *= f;
                     if (j > 0) {   // the product before is complete: this tile's scores were issued behind it
                         const uint64_t f2 = pair(f, f);
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < D; c += 16) {
                             uint32_t o[16];
                             tmem_load16(o, o_at + c);
@@ -617,7 +617,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
                 for (int t = 0; t < 8; ++t) odd |= it.odd[t / 4][t % 4];
                 E *out = (E *)a.out + (size_t)token * a.ldo + (size_t)head * D;
-#pragma unroll
+#pragma unroll 1   // little code: the tiles' own stays near
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
                     tmem_load32(o, o_at + c);

@@ -24,10 +24,18 @@ struct TreeArgs {
     unsigned int *errors;
     int n, T, Hkv, group, ldq, ldo, table_width, ld_table, max_draft, pages, page_shift;
     int whole;   // items are not cut: a run is of items
+    int tile_tokens;   // drafted tokens of a tensor-core tile: 128 / group of them, whole groups of rows
     float scale_log2;
 };
 
 constexpr int kMinTiles = 2;       // key tiles of a run, at least
+constexpr int kTreeTileRows = 256; // rows of an item on the tensor cores: two tiles of 128
+
+// The drafted token of row `local` of tile s of a block of two (-1: none); its head in the group is local % group.
+__device__ __forceinline__ int tile_token(const TreeArgs &a, int block, int s, int local, int m) {
+    const int t = local / a.group, token = (2 * block + s) * a.tile_tokens + t;
+    return t < a.tile_tokens && token < m ? token : -1;
+}
 
 // One sequence: its tokens, its keys and its work.
 struct Seq {
@@ -51,7 +59,8 @@ __device__ __forceinline__ Seq sequence(const TreeArgs &a, int s) {
     const int64_t room = min(((int64_t)a.table_width << a.page_shift) + 1, (int64_t)INT32_MAX - 256);
     q.len = (int)min((int64_t)max(a.lens[s], 0), room);
     q.tiles = max(1, (q.len + q.m + KEYS - 1) / KEYS);
-    q.row_tiles = (q.m * a.group + ROWS - 1) / ROWS;
+    if constexpr (ROWS == kTreeTileRows) q.row_tiles = (q.m + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens);
+    else q.row_tiles = (q.m * a.group + ROWS - 1) / ROWS;
     return q;
 }
 
@@ -143,9 +152,8 @@ __device__ __forceinline__ uint32_t finite_part(uint32_t two) {
     return two;
 }
 
-// Trees with many rows a key head, on the tensor cores: pages of at least 8 rows, query groups that divide 128;
-// one CTA an SM, partial results of kTreeTileRows rows.
-constexpr int kTreeTileRows = 256;
+// Trees with many rows a key head, on the tensor cores: pages of at least 8 rows, groups of at most 128; one CTA
+// an SM, partial results of kTreeTileRows rows.
 cudaError_t launch_tree_tiles(const TreeArgs &a, const fb_kv_cache &cache, bool pdl, cudaStream_t s);
 
 // [page][head][row][D] in boxes of 64 columns and `rows` rows of a page.

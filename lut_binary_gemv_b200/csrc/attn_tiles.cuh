@@ -166,11 +166,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 int kt1 = 0, hk = 0;
                 if (more) {
                     const Seq &q = c.q;
-                    const int rt = c.item % q.row_tiles, rows = q.m * a.group - rt * kBlock;
+                    const int rt = c.item % q.row_tiles;
                     hk = c.item / q.row_tiles;
                     kt1 = (int)min((int64_t)q.tiles, c.kt + r.span - c.pos);
                     const bool whole = c.kt == 0 && kt1 == q.tiles;
-                    it.n[0] = kt1 - c.kt, it.n[1] = rows > kTile ? kt1 - c.kt : 0;
+                    it.n[0] = kt1 - c.kt, it.n[1] = (2 * rt + 1) * a.tile_tokens < q.m ? kt1 - c.kt : 0;
                     it.first = q.first, it.len = q.len, it.block = rt, it.head = hk;
                     it.clean_from = max(q.len / kTile - c.kt, 0);
                     it.seq = c.s, it.m = q.m, it.kt0 = c.kt;
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         // where a cut item begins, the join learns where it lies and in which CTA it ends
                         const int64_t end = c.pos + q.tiles;
                         a.records[blockIdx.x] = make_int4((int)((r.begin + end - 1) / r.run) + 1, q.first, c.item,
-                                                          min(rows, kBlock) | q.row_tiles << 16);
+                                                          q.m | q.row_tiles << 16);
                     }
                 }
                 if (lane == 0) {
@@ -193,10 +193,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     if (!warp_wait(bars.q_free[s], (q_uses[s] & 1) ^ 1)) return false;
                     ++q_uses[s];
                     if (lane == 0) {
-                        barrier_expect(bar(bars.q_full[s]), kTileBytes<D>);
+                        barrier_expect(bar(bars.q_full[s]), a.tile_tokens * a.group * D * 2);
                         for (int x = 0; x < D / 64; ++x)
                             tile_copy(tiles + s * kTileBytes<D> + x * (kTile * 128), &q_map, 64 * x, hk * a.group,
-                                      it.first + (it.block * kBlock + s * kTile) / a.group, bar(bars.q_full[s]));
+                                      it.first + (2 * it.block + s) * a.tile_tokens, bar(bars.q_full[s]));
                     }
                     __syncwarp();
                     return true;
@@ -486,14 +486,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (!ok) break;
             if (items[slot].n[0] == 0) break;
             const int n = items[slot].n[s], clean_from = items[slot].clean_from;
-            const int row = items[slot].block * kBlock + s * kTile + local;
+            int row;                 // of the sequence; over a cache the row's drafted token, -1 where there is none
             uint64_t bits = 0;       // over a cache: the drafted tokens that the row sees
-            bool exists = true;
             if constexpr (kCache) {
                 const int m = items[slot].m;
-                exists = row < m * a.group;
-                if (exists) bits = a.mask ? a.mask[items[slot].first + row / a.group] : ~0ull >> (63 - row / a.group);
+                row = tile_token(a, items[slot].block, s, local, m);
+                if (row >= 0) bits = a.mask ? a.mask[items[slot].first + row] : ~0ull >> (63 - row);
                 if (m < 64) bits &= (1ull << m) - 1;
+            } else {
+                row = items[slot].block * kBlock + s * kTile + local;
             }
             float m = -INFINITY, l = 0.0f;   // m: the (scaled) maximum that the weights so far are relative to
             for (int j = 0; j < n; ++j) {
@@ -605,8 +606,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 int token, head, hk;
                 bool mine;
                 if constexpr (kCache) {
-                    token = first + row / a.group, hk = it.head, head = hk * a.group + row % a.group;
-                    mine = exists;
+                    token = first + row, hk = it.head, head = hk * a.group + local % a.group;
+                    mine = row >= 0;
                 } else {
                     token = first + row, head = it.head, hk = head / a.group;
                     mine = row < it.len;

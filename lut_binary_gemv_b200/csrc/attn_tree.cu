@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(kJoinThreads<ROWS>) join_kernel(const TreeArgs
     __shared__ float2 s_ml[kBlockThreads];
     wait_for_previous_kernel();
     const int4 rec = a.records[blockIdx.x];
-    const int row_tiles = rec.w >> 16, rows = rec.w & 0xFFFF;
+    const int row_tiles = rec.w >> 16, rows = rec.w & 0xFFFF;   // tensor-core tiles: the drafted tokens
     if (rec.x == 0) return;
     const int first = blockIdx.x, last = rec.x - 1, tid = threadIdx.x;
     const int units = kRowsBeside ? ROWS * CH : rows * CH;
@@ -550,7 +550,10 @@ __global__ void __launch_bounds__(kJoinThreads<ROWS>) join_kernel(const TreeArgs
     for (int u0 = blockIdx.y * at_once; u0 < units; u0 += gridDim.y * at_once) {
         const int unit = u0 + tid % at_once, share = tid / at_once;
         const int row = kRowsBeside ? unit % ROWS : unit / CH, c = kRowsBeside ? unit / ROWS : unit % CH;
-        const bool mine = unit < units && row < rows && share < shares;
+        const int hk = rec.z / row_tiles, rt = rec.z % row_tiles, rr = rt * ROWS + row;
+        const int token = kRowsBeside ? tile_token(a, rt, row / 128, row % 128, rows) : rr / a.group;
+        const int h = hk * a.group + (kRowsBeside ? row % 128 : rr) % a.group;
+        const bool mine = unit < units && share < shares && (kRowsBeside ? token >= 0 : row < rows);
         float top = -INFINITY, sum = 0.0f;
         float4 y = make_float4(0, 0, 0, 0);
         for (int x0 = first + share; mine && x0 <= last; x0 += kAtOnce * shares) {
@@ -594,14 +597,12 @@ __global__ void __launch_bounds__(kJoinThreads<ROWS>) join_kernel(const TreeArgs
             }
         }
         if (!mine || share > 0) continue;
-        const int hk = rec.z / row_tiles, rr = rec.z % row_tiles * ROWS + row;
-        const int token = rec.y + rr / a.group, h = hk * a.group + rr % a.group;
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         uint2 packed;
         packed.x = pack2<E>(y.x * inv, y.y * inv), packed.y = pack2<E>(y.z * inv, y.w * inv);
-        *reinterpret_cast<uint2 *>((E *)a.out + (size_t)token * a.ldo + (size_t)h * D + 4 * c) = packed;
+        *reinterpret_cast<uint2 *>((E *)a.out + (size_t)(rec.y + token) * a.ldo + (size_t)h * D + 4 * c) = packed;
         if (a.lse && c == 0)
-            a.lse[(size_t)token * a.Hkv * a.group + h] =
+            a.lse[(size_t)(rec.y + token) * a.Hkv * a.group + h] =
                 sum == 0.0f ? -INFINITY : ((top == -INFINITY ? 0.0f : top) + log2f(sum)) * 0.69314718056f;
     }
 }
@@ -614,7 +615,7 @@ struct Shape {
 };
 Shape shape_of(int Hq, const fb_kv_cache &c, int max_draft, int table_width) {
     const int group = Hq / c.Hkv, most = max_draft * group;
-    if (most > 32 && 128 % group == 0 && c.page_size >= 8) return {kTreeTileRows, sm_count(), true, false};
+    if (most > 32 && group <= 128 && c.page_size >= 8) return {kTreeTileRows, sm_count(), true, false};
     return {most <= 16 ? 16 : most <= 32 ? 32 : 64, sm_count() * kCtasPerSm, false,
             (int64_t)table_width * c.page_size <= kWholeKeys};
 }
@@ -728,6 +729,7 @@ extern "C" fb_status fb_attn_tree(const void *q, int ldq, int T, int Hq, const f
     a.errors = (unsigned int *)attn_errors_address();
     if (!a.errors) return FB_ERR_CUDA;
     a.whole = sh.whole;
+    a.tile_tokens = group <= 128 ? 128 / group : 0;
     const bool pdl = flags & FB_GEMV_PDL;
     cudaStream_t s = as_stream(stream);
     if (cache->t == FB_F16)

@@ -17,7 +17,7 @@ template <typename E, int D>
 cudaError_t launch_tiles(const TreeArgs &a, const fb_kv_cache &cache, bool pdl, cudaStream_t s) {
     CUtensorMap q, k, v;
     const int rows = cache.page_size < kTile ? cache.page_size : kTile;
-    if (!head_map(&q, a.q, cache.t, a.T, a.Hkv * a.group, D, a.ldq, a.group, kTile / a.group) ||
+    if (!head_map(&q, a.q, cache.t, a.T, a.Hkv * a.group, D, a.ldq, a.group, a.tile_tokens) ||
         !cache_map(&k, cache.k, cache, rows) || !cache_map(&v, cache.v, cache, rows))
         return cudaErrorInvalidValue;
     if (!registers_as_planned<tile_kernel<E, D, TreeArgs>>()) return cudaErrorInvalidValue;

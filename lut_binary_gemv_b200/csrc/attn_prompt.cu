@@ -12,21 +12,35 @@
 namespace fb {
 namespace {
 
-template <typename E, int D>
-cudaError_t launch_prompt(const PromptArgs &a, const fb_heads &in, bool pdl, cudaStream_t s) {
+// Up to this many full items for ten SMs, items are split.  Measured, split and not: 150 items, the longest of
+// 12,066 keys, 95 and 148 us; 75 items of up to 3,431 keys 30 and 47; 128 even items of 1,000 25 and 23; 256 even
+// items of 4,096 92 and 71 (each key tile then serves half as many queries).
+constexpr int kSplitItems = 11;
+
+
+template <typename E, int D, typename Args>
+cudaError_t launch_items(const Args &a, int64_t most, const fb_heads &in, bool pdl, cudaStream_t s) {
     CUtensorMap q, k, v;
     if (!head_map(&q, in.q, in.t, in.T, in.Hq, D, in.ldq, 1, kTile) ||
         !head_map(&k, in.k, in.t, in.T, in.Hkv, D, in.ldk, 1, kTile) ||
         !head_map(&v, in.v, in.t, in.T, in.Hkv, D, in.ldv, 1, kTile))
         return cudaErrorInvalidValue;
-    auto kernel = tile_kernel<E, D, PromptArgs>;
-    if (!registers_as_planned<tile_kernel<E, D, PromptArgs>>()) return cudaErrorInvalidValue;   // a warp would wait for registers for good
-    cudaError_t e = allow_shared<tile_kernel<E, D, PromptArgs>>(kSmemBytes<D>);
+    // a warp would wait for registers for good
+    if (!registers_as_planned<tile_kernel<E, D, Args>>()) return cudaErrorInvalidValue;
+    const cudaError_t e = allow_shared<tile_kernel<E, D, Args>>(kSmemBytes<D>);
     if (e != cudaSuccess) return e;
     // one CTA an SM, no more than there can be items
-    const int64_t most = ((int64_t)(in.T + kBlock - 1) / kBlock + (a.n < in.T ? a.n : in.T)) * in.Hq;
     const int ctas = (int)(most < sm_count() ? most : sm_count());
-    return launch(kernel, dim3(ctas), dim3(kTileThreads), kSmemBytes<D>, s, pdl, a, q, k, v);
+    return launch(tile_kernel<E, D, Args>, dim3(ctas), dim3(kTileThreads), kSmemBytes<D>, s, pdl, a, q, k, v);
+}
+
+// Items of 256 queries where they go round the SMs, else of 128, split over their keys.
+template <typename E, int D>
+cudaError_t launch_prompt(const PromptArgs &a, const fb_heads &in, bool pdl, cudaStream_t s) {
+    const int64_t n = a.n < in.T ? a.n : in.T, blocks = (in.T + kBlock - 1) / kBlock;
+    if (blocks * in.Hq * 10 <= kSplitItems * (int64_t)sm_count())
+        return launch_items<E, D>(SplitArgs{a}, ((in.T + kTile - 1) / kTile + n) * in.Hq, in, pdl, s);
+    return launch_items<E, D>(a, (blocks + n) * in.Hq, in, pdl, s);
 }
 
 }  // namespace

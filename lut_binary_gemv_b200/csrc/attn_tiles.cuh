@@ -78,6 +78,10 @@ struct PromptArgs {
     float scale_log2;
 };
 
+// Few items for the CTAs: an item is one tile of queries, and the two tiles' places take its key tiles in turn
+// (even ones, odd ones), which halves the longest item; their results are joined in tensor memory at the end.
+struct SplitArgs : PromptArgs {};
+
 struct Item {
     int n[2];                      // tiles of keys that the two query tiles meet; n[0] 0: no more items
     int first, len, block, head;   // the sequence's first token and (committed) length; the block of 256 rows; the
@@ -92,6 +96,7 @@ struct Barriers {
     uint64_t full[8], free_[8], clean[8], ask[8];   // the ring
     uint64_t s_full[2], p_full[2][2], o_full[2];   // the weights by halves of the keys
     uint64_t item_full[kItems], item_free[kItems];
+    uint64_t merge_full, merge_free;        // the second half of a split item there, read
     uint64_t done;
 };
 
@@ -100,18 +105,20 @@ static_assert(kBlock == kTreeTileRows, "the join reads the blocks' rows");
 // What starting and ending an item costs, in key tiles.
 constexpr int kTilePiece = 3;
 
-// Args: PromptArgs for packed prompts, TreeArgs for drafted trees over a paged cache (rows: the drafted tokens
+// Args: PromptArgs or SplitArgs for packed prompts, TreeArgs for drafted trees over a paged cache (rows: the drafted tokens
 // times the query heads of a key head).
 template <typename E, int D, typename Args>
 __global__ void __launch_bounds__(kTileThreads, 1)
     tile_kernel(const Args a, const __grid_constant__ CUtensorMap q_map,
                   const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     constexpr int R = kRing<D>;
-    constexpr bool kCache = std::is_same_v<Args, TreeArgs>;
+    constexpr bool kCache = std::is_same_v<Args, TreeArgs>, kSplit = std::is_same_v<Args, SplitArgs>;
+    constexpr int kRows = kSplit ? kTile : kBlock;   // of an item
     constexpr bool kBf16 = std::is_same_v<E, __nv_bfloat16>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) Barriers bars;
     __shared__ Item items[kItems];
+    __shared__ float2 merge_ml[kSplit ? kTile : 1];   // maxima and sums of the second half
     __shared__ uint32_t tmem_at;
     __shared__ int gave_up_word;
     volatile int *gave_up = &gave_up_word;
@@ -137,6 +144,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         for (int i = 0; i < kItems; ++i)
             barrier_init(bar(bars.item_full[i]), 1), barrier_init(bar(bars.item_free[i]), kItemReaders);
+        barrier_init(bar(bars.merge_full), 4), barrier_init(bar(bars.merge_free), 4);
         barrier_init(bar(bars.done), 1);
         barrier_inits_done();
     }
@@ -260,7 +268,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         first = min(max(a.cu[base + lane], 0), a.T);
                         len = min(max(a.cu[base + lane + 1], first), a.T) - first;
                     }
-                    blocks = (len + kBlock - 1) / kBlock;
+                    blocks = (len + kRows - 1) / kRows;
                     chunk = (int64_t)__reduce_add_sync(~0u, blocks) * a.Hq;
                     level = __reduce_max_sync(~0u, blocks) - 1;
                     level_before = 0;
@@ -278,9 +286,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     it.first = __shfl_sync(~0u, first, src), it.len = __shfl_sync(~0u, len, src);
                     it.head = i % a.Hq;
                     it.block = level;
-                    it.n[0] = 2 * level + 1;
-                    it.n[1] = level * kBlock + kTile < it.len ? 2 * level + 2 : 0;
-                    it.clean_from = 2 * level;
+                    if (kSplit) {
+                        it.n[0] = (level + 2) / 2, it.n[1] = (level + 1) / 2;
+                        it.clean_from = level;
+                    } else {
+                        it.n[0] = 2 * level + 1;
+                        it.n[1] = level * kBlock + kTile < it.len ? 2 * level + 2 : 0;
+                        it.clean_from = 2 * level;
+                    }
                 }
                 const int slot = count % kItems;
                 bool ok = true;
@@ -298,7 +311,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             barrier_expect(bar(bars.q_full[s]), kTileBytes<D>);
                             for (int c = 0; c < D / 64; ++c)
                                 tile_copy(tiles + s * kTileBytes<D> + c * (kTile * 128), &q_map, 64 * c, it.head,
-                                          it.first + it.block * kBlock + s * kTile, bar(bars.q_full[s]));
+                                          it.first + it.block * kRows + s * kTile, bar(bars.q_full[s]));
                             return true;
                         };
                         auto load_ring = [&](const CUtensorMap *map, int tile, bool ask) {
@@ -312,9 +325,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             if (ask) barrier_arrive(bar(bars.ask[place]));
                             return true;
                         };
-                        ok = load_query(0) && load_ring(&k_map, 0, false) && (n1 == 0 || load_query(1));
-                        for (int j = 0; ok && j < n; ++j)
-                            ok = (j == 0 || load_ring(&k_map, j, false)) && load_ring(&v_map, j, j >= it.clean_from);
+                        if (kSplit) {   // the keys two tiles ahead of the values
+                            const int all = it.n[0] + n1;
+                            ok = load_query(0) && load_ring(&k_map, 0, false) && (all == 1 || load_ring(&k_map, 1, false));
+                            for (int j = 0; ok && j < all; ++j)
+                                ok = load_ring(&v_map, j, j == all - 1) && (j + 2 >= all || load_ring(&k_map, j + 2, false));
+                        } else {
+                            ok = load_query(0) && load_ring(&k_map, 0, false) && (n1 == 0 || load_query(1));
+                            for (int j = 0; ok && j < n; ++j)
+                                ok = (j == 0 || load_ring(&k_map, j, false)) && load_ring(&v_map, j, j >= it.clean_from);
+                        }
                     }
                 }
                 if (!__shfl_sync(~0u, (int)ok, 0) || it.n[0] == 0) break;
@@ -335,7 +355,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         Place place = {0, 0};
         uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0}, clean_phase = 0;   // clean_phase: a bit a place
         auto scores = [&](int s, uint32_t at) {
-            const uint32_t q = tile_descriptor(tiles + s * kTileBytes<D>, 16);
+            const uint32_t q = tile_descriptor(tiles + (kSplit ? 0 : s) * kTileBytes<D>, 16);
             const uint32_t k = tile_descriptor(ring + at * kTileBytes<D>, 16);
             if (leader) {
 #pragma unroll
@@ -367,6 +387,55 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 __syncwarp();
                 if (leader) barrier_arrive(bar(bars.item_free[slot]));
                 if (n0 == 0) return;
+                if constexpr (kSplit) {
+                    const int all = n0 + n1;
+                    if (!warp_wait(bars.q_full[0], q_phase[0])) return;
+                    q_phase[0] ^= 1;
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        if (s >= all) continue;
+                        if (!warp_wait(bars.full[place.at], place.phase)) return;
+                        tensor_fence_after();
+                        scores(s, place.at);
+                        commit(bars.free_[place.at]);
+                        place.next();
+                    }
+                    if (all <= 2) commit(bars.q_free[0]);
+                    for (int t0 = 0; t0 < all; t0 += 2) {
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {
+                            const int t = t0 + s;
+                            if (t >= all) continue;
+                            const bool more = t + 2 < all;
+                            const Place v = place;
+                            place.next();
+                            const Place k = place;   // the keys two tiles on
+                            if (more) place.next();
+                            if (!warp_wait(bars.full[v.at], v.phase)) return;
+                            if (t == all - 1) {
+                                if (!warp_wait(bars.clean[v.at], clean_phase >> v.at & 1)) return;
+                                clean_phase ^= 1u << v.at;
+                            }
+                            if (more && !warp_wait(bars.full[k.at], k.phase)) return;
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                if (!warp_wait(bars.p_full[s][h], p_phase[s])) return;
+                                tensor_fence_after();
+                                values(s, v.at, h, t0 > 0 || h > 0);
+                            }
+                            p_phase[s] ^= 1;
+                            if (more) {
+                                scores(s, k.at);
+                                if (t + 3 == all) commit(bars.q_free[0]);
+                            } else {
+                                commit(bars.o_full[s]);
+                            }
+                            commit(bars.free_[v.at]);
+                            if (more) commit(bars.free_[k.at]);
+                        }
+                    }
+                    continue;
+                }
                 if (!warp_wait(bars.full[place.at], place.phase)) return;
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
@@ -426,7 +495,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             const int slot = count % kItems;
             ok = warp_wait(bars.item_full[slot], count / kItems & 1);
             if (!ok) break;
-            const int n0 = items[slot].n[0], n = max(n0, items[slot].n[1]), from = items[slot].clean_from;
+            const int n0 = items[slot].n[0], n1 = items[slot].n[1], n = kSplit ? n0 + n1 : max(n0, n1);
+            const int from = items[slot].clean_from;
             // keys of the tile, counted from the first tile looked at
             const int keys = items[slot].len + items[slot].m - (kCache ? items[slot].len / kTile : from) * kTile;
             const int skip = kCache ? items[slot].kt0 + from - items[slot].len / kTile : 0;
@@ -474,7 +544,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
         const uint32_t s_at = tmem + lanes + s * kTile, o_at = tmem + lanes + 2 * kTile + s * D;
         const uint64_t scale2 = pair(a.scale_log2, a.scale_log2);
-        uint32_t s_uses = 0, o_uses = 0;
+        uint32_t s_uses = 0, o_uses = 0, merges = 0;
         const int heads = [&] {
             if constexpr (kCache) return a.Hkv * a.group;
             else return a.Hq;
@@ -494,7 +564,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 if (row >= 0) bits = a.mask ? a.mask[items[slot].first + row] : ~0ull >> (63 - row);
                 if (m < 64) bits &= (1ull << m) - 1;
             } else {
-                row = items[slot].block * kBlock + s * kTile + local;
+                row = items[slot].block * kRows + (kSplit ? 0 : s * kTile) + local;
             }
             float m = -INFINITY, l = 0.0f;   // m: the (scaled) maximum that the weights so far are relative to
             for (int j = 0; j < n; ++j) {
@@ -502,7 +572,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 if (!ok) break;
                 tensor_fence_after();
                 uint32_t x[4][32];
-                const bool diagonal = kCache ? j >= clean_from : j == n - 1;   // some row must not see some key
+                // some row must not see some key (of a split item, the last tile alone lies on the diagonal)
+                const bool diagonal = kCache ? j >= clean_from : j == n - 1 && (!kSplit || s == (clean_from & 1));
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_load32(x[c], s_at + 32 * c);
 #pragma unroll
@@ -597,7 +668,23 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 unpair(add2(sum[0], sum[1]), lo, hi);
                 l += lo + hi;
             }
-            if (ok && n > 0) {
+            bool second = false;   // a split item's second half, to be joined to the first
+            if constexpr (kSplit) {
+                if (ok && n > 0 && s == 1) {
+                    merge_ml[local] = make_float2(m, l);
+                    __syncwarp();
+                    if (lane == 0) barrier_arrive(bar(bars.merge_full));
+                    ok = warp_wait(bars.merge_free, merges++ & 1);   // its outputs stay until they have been read
+                    if (!ok) break;
+                }
+                second = s == 0 && items[slot].n[1] > 0;
+                if (ok && second) {
+                    ok = warp_wait(bars.o_full[1], merges & 1) && warp_wait(bars.merge_full, merges & 1);
+                    ++merges;
+                    if (!ok) break;
+                }
+            }
+            if (ok && n > 0 && !(kSplit && s == 1)) {
                 ok = warp_wait(bars.o_full[s], o_uses++ & 1);
                 if (!ok) break;
                 tensor_fence_after();
@@ -613,6 +700,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     mine = row < it.len;
                 }
                 const bool partial = kCache && it.piece >= 0;
+                float f0 = 1.0f, f1 = 0.0f;   // of the halves of a split item
+                if (kSplit && second) {
+                    const float2 other = merge_ml[kSplit ? local : 0];
+                    const float best = fmaxf(m, other.x), ref = best == -INFINITY ? 0.0f : best;
+                    f0 = exp2_approx(m - ref), f1 = exp2_approx(other.x - ref);
+                    l = l * f0 + other.y * f1, m = ref;
+                }
                 const float inv = partial ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
                 uint32_t odd = 0;
 #pragma unroll
@@ -624,7 +718,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     tmem_load32(o, o_at + c);
                     tmem_wait32(o);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * (kSplit ? f0 * inv : inv));
+                    if (kSplit && second) {
+                        uint32_t o1[32];
+                        tmem_load32(o1, o_at + D + c);
+                        tmem_wait32(o1);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            o[i] = __float_as_uint(fmaf(__uint_as_float(o1[i]), f1 * inv, __uint_as_float(o[i])));
+                    }
                     for (int t = 0; odd && t < 2; ++t)
                         for (int w = 0; w < 4; ++w)
                             for (uint32_t rows = it.odd[t][w]; rows; rows &= rows - 1) {
@@ -638,7 +740,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                                         v = (const E *)a.vc + ((((size_t)page * a.Hkv + hk) << a.page_shift) +
                                                                (key & ((1 << a.page_shift) - 1))) * D + c;
                                 } else {
-                                    const int key = (2 * it.block + t) * kTile + 32 * w + __ffs(rows) - 1;
+                                    const int key = (kRows / kTile * it.block + t) * kTile + 32 * w + __ffs(rows) - 1;
                                     if (key > row) continue;
                                     v = (const E *)a.v + (size_t)(first + key) * a.ldv + (size_t)hk * D + c;
                                 }
@@ -671,6 +773,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     }
                 }
                 tensor_fence_before();
+                if (kSplit && second) {
+                    __syncwarp();
+                    if (lane == 0) barrier_arrive(bar(bars.merge_free));
+                }
                 if (partial && mine) {
                     if constexpr (kCache)
                         *reinterpret_cast<float2 *>(a.part_ml + ((size_t)it.piece * kBlock + s * kTile + local) * 2) = make_float2(m, l);

@@ -233,15 +233,20 @@ PROMPTS = [
 ]
 
 
+# with few items (split over their keys) and with as many as go round the SMs
+@pytest.mark.parametrize("times", [1, 300])
 @pytest.mark.parametrize("case", PROMPTS, ids=lambda c: f"{len(c[0])}x{max(c[0])}-{c[1]}/{c[2]}-{c[3]}-{str(c[4])[6:]}")
-def test_prompt(case):
+def test_prompt(case, times):
     lens, Hq, Hkv, D, dtype, tail, fused = case
+    group, Hkv = Hq // Hkv, Hkv * -(-times // Hq)
+    Hq = Hkv * group
     q, k, v, cu, cud = prompt_inputs(lens, Hq, Hkv, D, dtype, tail, seed=sum(lens), fused=fused)
     out = torch.full((q.shape[0], Hq, D), 7.5, dtype=dtype, device=DEV)
     lse = torch.full((q.shape[0], Hq), -3.25, device=DEV)
     scale = 0.9 * D ** -0.5
     assert fb.fb_attn_prompt(q, k, v, cud, scale, out, lse) is out
-    check_attention(out, lse, prompt_refs(q, k, v, cu, scale), D, dtype, "prompt")
+    heads = None if times == 1 else [0, Hq // 2, Hq - 1]
+    check_attention(out, lse, prompt_refs(q, k, v, cu, scale, heads), D, dtype, "prompt")
     assert (out[cu[-1]:] == 7.5).all() and (lse[cu[-1]:] == -3.25).all()
     again = fb.fb_attn_prompt(q, k, v, cud, scale)
     assert torch.equal(again[:cu[-1]], out[:cu[-1]])                    # deterministic; lse not needed
@@ -256,26 +261,28 @@ def test_prompt_longer_one_head():
     check_attention(out, lse, prompt_refs(q, k, v, cu, 128 ** -0.5, heads=[1]), 128, torch.bfloat16, "long")
 
 
+@pytest.mark.parametrize("H", [1, 128])
 @pytest.mark.parametrize("D", [64, 128])
-def test_prompt_rising_scores(D):
+def test_prompt_rising_scores(D, H):
     # every key scores above all earlier ones by 3 (base e): the running maximum moves at every key
     n = 700
-    q = torch.zeros(n, 1, D, dtype=torch.float16, device=DEV)
-    k = torch.zeros_like(q)
+    q = torch.zeros(n, H, D, dtype=torch.float16, device=DEV)
+    k = torch.zeros(n, 1, D, dtype=torch.float16, device=DEV)
     q[..., 0] = 1.0
     k[..., 0] = (torch.arange(n, device=DEV) * 3.0)[:, None].half()
     v = normal(gen(1), n, 1, D, dtype=torch.float16)
     cud = torch.tensor([0, n], dtype=torch.int32, device=DEV)
-    lse = torch.empty(n, 1, device=DEV)
+    lse = torch.empty(n, H, device=DEV)
     out = fb.fb_attn_prompt(q, k, v, cud, 1.0, lse=lse)
-    check_attention(out, lse, prompt_refs(q, k, v, [0, n], 1.0), D, torch.float16, "rising")
+    check_attention(out, lse, prompt_refs(q, k, v, [0, n], 1.0, heads=[H - 1]), D, torch.float16, "rising")
     out = fb.fb_attn_prompt(q, k.flip(0).contiguous(), v, cud, 1.0, lse=lse)
-    check_attention(out, lse, prompt_refs(q, k.flip(0), v, [0, n], 1.0), D, torch.float16, "falling")
+    check_attention(out, lse, prompt_refs(q, k.flip(0), v, [0, n], 1.0, heads=[0]), D, torch.float16, "falling")
 
 
+@pytest.mark.parametrize("Hkv", [2, 160])
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
-def test_prompt_special_values_reach_only_rows_that_see_them(value):
-    lens, Hq, Hkv, D = [200, 61, 300], 4, 2, 128
+def test_prompt_special_values_reach_only_rows_that_see_them(value, Hkv):
+    lens, Hq, D = [200, 61, 300], 2 * Hkv, 128
     q, k, v, cu, cud = prompt_inputs(lens, Hq, Hkv, D, torch.bfloat16, tail=9, seed=8)
     ref = fb.fb_attn_prompt(q, k, v, cud)
     at = 230                                             # in the second sequence
@@ -293,7 +300,7 @@ def test_prompt_special_values_reach_only_rows_that_see_them(value):
     k2[-1] = value
     got = fb.fb_attn_prompt(q, k2, v, cud)
     hit[:] = False
-    hit[at:261, 2:] = True
+    hit[at:261, 2:4] = True
     assert torch.equal(got[:561][~hit[:561]], ref[:561][~hit[:561]]) and bool(torch.isnan(got[hit]).all())
 
 

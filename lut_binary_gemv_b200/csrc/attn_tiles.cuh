@@ -26,7 +26,14 @@
 // Tensor memory: two score tiles of 128 columns, each overwritten by its
 // weights (64 columns), and two outputs of D columns.  The products are issued
 // by one thread and complete in order, so a new score tile may be asked for as
-// soon as the product that reads the old weights has been issued.
+// soon as the product that reads the old weights has been issued.  The weights
+// come in two halves, so that the product starts before the second is there.
+//
+// Measured (16,384 tokens, 32 heads over 8 of 128, bf16): 1.69 ms, 1.30 PFLOP/s,
+// tensor cores 66% busy; a step of 128 keys and 256 queries takes 3,250 cycles:
+// the chain of one tile (scores, 1,950 cycles of softmax, product, scores) is
+// what two tiles in turn do not quite hide.  K and V come from L2 (5.5 GB a
+// launch), not from HBM.
 //
 // The outputs are rescaled only when a row's maximum has grown by more than
 // 2^8 since the last time (exact all the same: the sum carries the same factor,

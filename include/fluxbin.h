@@ -306,8 +306,8 @@ FB_API fb_status fb_fit_base(float *R, int M, int N, int ldr, int sweeps, int8_t
  * `stream`, deterministic, and keep every norm, score, softmax sum and
  * accumulated output in fp32.  flags: 0 or FB_GEMV_PDL (the kernel may be
  * launched before the previous one ends; it reads and writes nothing before
- * that one has completed).  Pointers are 16-byte aligned unless stated
- * otherwise, row pitches (ld*, in elements) multiples of 16 bytes.
+ * that one has completed); arrays that a call reads must keep their values
+ * until it is done.  Pointers are 16-byte aligned unless stated otherwise, row pitches (ld*, in elements) multiples of 16 bytes.
  * Limits: 1 <= T <= 2^24, 1 <= Hq <= 1024, Hkv divides Hq. */
 
 /* The heads of T tokens: head h of token i is the D consecutive elements at

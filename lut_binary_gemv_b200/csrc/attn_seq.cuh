@@ -107,7 +107,8 @@ __device__ __forceinline__ Run find_run(const TreeArgs &a, Cursor &at) {
     r.begin = r.run * blockIdx.x, r.span = min(r.run, total - r.begin);
     if (r.span <= 0) return r;
     int64_t before = 0;
-    for (int base = 0;; base += 32) {
+    int base = 0;
+    for (; base < a.n; base += 32) {
         const int64_t w = base + lane < a.n ? weight(base + lane) : 0;
         int64_t upto = w;
 #pragma unroll
@@ -123,6 +124,10 @@ __device__ __forceinline__ Run find_run(const TreeArgs &a, Cursor &at) {
             break;
         }
         before += __shfl_sync(~0u, upto, 31);
+    }
+    if (base >= a.n) {   // only if the lengths changed under the call: no work, rather than a search without end
+        r.span = 0;
+        return r;
     }
     at.q = sequence<ROWS, KEYS>(a, at.s);
     if (a.whole) {

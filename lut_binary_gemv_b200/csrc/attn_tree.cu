@@ -406,6 +406,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     odd |= not_finite<E>(v.x) || not_finite<E>(v.y) || not_finite<E>(v.z) || not_finite<E>(v.w);
                 }
                 writes_before_async();
+                if (kOwnKeys) __syncwarp();   // other lanes read the cleared rows, and a vote orders no memory
                 odd = kOwnKeys ? __any_sync(~0u, odd) : __syncthreads_or(odd);
                 if (odd) {
                     for (int kk = 0; kk < KW; ++kk) {

@@ -482,6 +482,19 @@ def test_tree_masks_that_leave_nothing_or_holes():
         assert not out[row].any() and bool((lse[row] == -float("inf")).all())
 
 
+@pytest.mark.parametrize("garbage", [float("nan"), float("inf")])
+@pytest.mark.parametrize("Hq,D,page_size,dtype", [(1, 64, 16, torch.float16), (1, 128, 16, torch.bfloat16),
+                                                  (20, 64, 64, torch.bfloat16), (20, 128, 4, torch.float16)])
+def test_tree_values_behind_the_keys_reach_no_row(Hq, D, page_size, dtype, garbage):
+    # every place of the last key within a tile and within a warp's keys, the values behind it not finite
+    c = tree_inputs(list(range(130)), [1] * 130, Hq, 1, D, page_size, dtype, seed=41, garbage=garbage)
+    out, lse = tree_call(c, None)
+    check_attention(out, lse, tree_refs(c, None, D ** -0.5, heads=[0, Hq - 1]), D, dtype, "behind")
+    for _ in range(20):
+        again, _ = tree_call(c, None)
+        assert torch.equal(again, out)
+
+
 # up to 16 rows a key head, up to 32, more by each path
 @pytest.mark.parametrize("Hq,page_size", [(2, 16), (2, 4), (8, 16), (8, 4)])
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])

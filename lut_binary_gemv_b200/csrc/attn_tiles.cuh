@@ -797,9 +797,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     __syncthreads();
     if (gave_up_word) {
-        // copies and products that were under way land in this CTA's memory: give them time before it is reused
-        const uint64_t start = now_ns();
-        while (now_ns() - start < 20000000ull) __nanosleep(1000);
+        outlast_copies();
         if (tid == 0) atomicOr(a.errors, kErrorWait);
         __syncthreads();
     }

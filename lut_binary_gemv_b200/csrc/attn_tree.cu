@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // ---- loading: each warp brings in keys 16 warp .. 16 warp + 15 of a tile ----
     Cursor ahead = at;
     int load_stage = 0;
+    bool lost = false;   // a wait was given up: no more copies, whose places may still be awaiting the last ones
     // the page of a key position of the cursor's sequence (-1 beyond the table)
     auto page_of = [&](int p) {
         const int slot = p >> a.page_shift;
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     };
     int page = page_of(ahead.kt * kTileKeys + 16 * warp + (kTiled ? 0 : lane % 16));   // looked up a tile early
     auto load_tile = [&]() {
-        if (ahead.pos < span) {
+        if (ahead.pos < span && !lost) {
             const int hk = ahead.item / ahead.q.row_tiles, keys = ahead.q.len + ahead.q.m;
             const uint32_t k_at = stages + load_stage * kStageBytes<D> + warp * kSlice<D>, v_at = k_at + kHalf;
             const int p0 = ahead.kt * kTileKeys + 16 * warp;
@@ -281,17 +282,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         for (int t = 0; t < MT; ++t) m[t][0] = m[t][1] = -INFINITY, l[t][0] = l[t][1] = 0.0f;
 
         for (int kt = kt0; kt < kt1; ++kt) {
+            bool there = true;
             if constexpr (kTiled) {
                 if (kOwnKeys) {
-                    barrier_wait(smem_address(&full[stage][warp]), phase, gave_up);
+                    there = barrier_wait(smem_address(&full[stage][warp]), phase, gave_up);
                 } else {
-                    for (int i = 0; i < KW / 16; ++i) barrier_wait(smem_address(&full[stage][wk * (KW / 16) + i]), phase, gave_up);
+                    for (int i = 0; i < KW / 16; ++i) there &= barrier_wait(smem_address(&full[stage][wk * (KW / 16) + i]), phase, gave_up);
                 }
             } else {
                 copies_wait<S - 2>();
             }
-            if (kOwnKeys) __syncwarp();
-            else __syncthreads();
+            if (kOwnKeys) {
+                __syncwarp();
+                if (kTiled) lost |= !__all_sync(~0u, there);
+            } else {
+                lost |= !__syncthreads_and(there);
+            }
             load_tile();   // into the place of the tile before, which its readers have left
             const uint32_t keys_at = stages + stage * kStageBytes<D> + wk * (KW / 16) * kSlice<D>, values_at = keys_at + kHalf;
 
@@ -531,7 +537,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
     }
     if (!kTiled) copies_wait<0>();
-    if (gave_up_word && tid == 0) atomicOr(a.errors, kErrorWait);
+    if (lost) {
+        outlast_copies();
+        if (lane == 0) atomicOr(a.errors, kErrorWait);
+    }
 }
 
 // Joins the pieces of the cut items: block x the one that begins in CTA x.  A thread takes four columns of a row;

@@ -64,6 +64,13 @@ __device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t parity, vola
     }
 }
 
+// After a wait was given up: copies and products that are under way land in this CTA's memory, so a thread stays a
+// while (20 ms) before the memory goes to another CTA.
+__device__ __forceinline__ void outlast_copies() {
+    const uint64_t start = now_ns();
+    while (now_ns() - start < 20000000ull) __nanosleep(1000);
+}
+
 // ---- tiled copies ------------------------------------------------------------------
 
 // One box of a [token][head][D] map: 64 columns from `col`, one head, the box's tokens from `token` on.

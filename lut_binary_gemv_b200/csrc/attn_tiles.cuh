@@ -162,387 +162,388 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t tmem = tmem_at;
     wait_for_previous_kernel();
 
-    if (warp == 8) {
-        // ---- items and copies -----------------------------------------------------
+    // Registers move by warpgroups: the four warps of one execute the same instruction, before their roles part.
+    if (warp >= 8) {
         give_registers<kFewRegisters>();
-        if constexpr (kCache) {
-            // A run of the list of key tiles, piece by piece.  The whole warp takes part: each lane looks up the
-            // page of its box (page_size keys, at most a tile) and copies it.
-            Cursor c;
-            const Run r = find_run<kBlock, kTile, kTilePiece>(a, c);
-            if (lane == 0) a.records[blockIdx.x] = make_int4(0, 0, 0, 0);
-            const int box = min(1 << a.page_shift, kTile), boxes = kTile / box;
-            uint32_t loads = 0, q_uses[2] = {0, 0};
-            bool more = r.span > 0;
-            for (uint32_t count = 0;; ++count) {
-                const int slot = count % kItems;
-                if (!warp_wait(bars.item_free[slot], (count / kItems & 1) ^ 1)) break;
-                Item it = {};
-                int kt1 = 0, hk = 0;
-                if (more) {
-                    const Seq &q = c.q;
-                    const int rt = c.item % q.row_tiles;
-                    hk = c.item / q.row_tiles;
-                    kt1 = (int)min((int64_t)q.tiles, c.kt + r.span - c.pos);
-                    const bool whole = c.kt == 0 && kt1 == q.tiles;
-                    it.n[0] = kt1 - c.kt, it.n[1] = (2 * rt + 1) * a.tile_tokens < q.m ? kt1 - c.kt : 0;
-                    it.first = q.first, it.len = q.len, it.block = rt, it.head = hk;
-                    it.clean_from = max(q.len / kTile - c.kt, 0);
-                    it.seq = c.s, it.m = q.m, it.kt0 = c.kt;
-                    it.piece = whole ? -1 : 2 * (int)blockIdx.x + (c.kt == 0 ? 1 : 0);
-                    if (!whole && c.kt == 0 && lane == 0) {
-                        // where a cut item begins, the join learns where it lies and in which CTA it ends
-                        const int64_t end = c.pos + q.tiles;
-                        a.records[blockIdx.x] = make_int4((int)((r.begin + end - 1) / r.run) + 1, q.first, c.item,
-                                                          q.m | q.row_tiles << 16);
+        if (warp == 8) {
+            // ---- items and copies -----------------------------------------------------
+            if constexpr (kCache) {
+                // A run of the list of key tiles, piece by piece.  The whole warp takes part: each lane looks up the
+                // page of its box (page_size keys, at most a tile) and copies it.
+                Cursor c;
+                const Run r = find_run<kBlock, kTile, kTilePiece>(a, c);
+                if (lane == 0) a.records[blockIdx.x] = make_int4(0, 0, 0, 0);
+                const int box = min(1 << a.page_shift, kTile), boxes = kTile / box;
+                uint32_t loads = 0, q_uses[2] = {0, 0};
+                bool more = r.span > 0;
+                for (uint32_t count = 0;; ++count) {
+                    const int slot = count % kItems;
+                    if (!warp_wait(bars.item_free[slot], (count / kItems & 1) ^ 1)) break;
+                    Item it = {};
+                    int kt1 = 0, hk = 0;
+                    if (more) {
+                        const Seq &q = c.q;
+                        const int rt = c.item % q.row_tiles;
+                        hk = c.item / q.row_tiles;
+                        kt1 = (int)min((int64_t)q.tiles, c.kt + r.span - c.pos);
+                        const bool whole = c.kt == 0 && kt1 == q.tiles;
+                        it.n[0] = kt1 - c.kt, it.n[1] = (2 * rt + 1) * a.tile_tokens < q.m ? kt1 - c.kt : 0;
+                        it.first = q.first, it.len = q.len, it.block = rt, it.head = hk;
+                        it.clean_from = max(q.len / kTile - c.kt, 0);
+                        it.seq = c.s, it.m = q.m, it.kt0 = c.kt;
+                        it.piece = whole ? -1 : 2 * (int)blockIdx.x + (c.kt == 0 ? 1 : 0);
+                        if (!whole && c.kt == 0 && lane == 0) {
+                            // where a cut item begins, the join learns where it lies and in which CTA it ends
+                            const int64_t end = c.pos + q.tiles;
+                            a.records[blockIdx.x] = make_int4((int)((r.begin + end - 1) / r.run) + 1, q.first, c.item,
+                                                              q.m | q.row_tiles << 16);
+                        }
                     }
-                }
-                if (lane == 0) {
-                    items[slot] = it;
-                    barrier_arrive(bar(bars.item_full[slot]));
-                }
-                __syncwarp();
-                if (!more) break;
-                const int keys = it.len + it.m;
-                auto load_query = [&](int s) {
-                    if (!warp_wait(bars.q_free[s], (q_uses[s] & 1) ^ 1)) return false;
-                    ++q_uses[s];
                     if (lane == 0) {
-                        barrier_expect(bar(bars.q_full[s]), a.tile_tokens * a.group * D * 2);
-                        for (int x = 0; x < D / 64; ++x)
-                            tile_copy(tiles + s * kTileBytes<D> + x * (kTile * 128), &q_map, 64 * x, hk * a.group,
-                                      it.first + (2 * it.block + s) * a.tile_tokens, bar(bars.q_full[s]));
-                    }
-                    __syncwarp();
-                    return true;
-                };
-                auto load_ring = [&](const CUtensorMap *map, int j, bool ask) {
-                    const int place = loads % R, p = (it.kt0 + j) * kTile + lane * box;
-                    const bool wanted = lane < boxes && p < keys;
-                    const int at = p >> a.page_shift;
-                    const int page = wanted && at < a.table_width ? a.table[(size_t)it.seq * a.ld_table + at] : -1;
-                    const bool good = wanted && page >= 0 && page < a.pages;
-                    if (!warp_wait(bars.free_[place], (loads / R & 1) ^ 1)) return false;
-                    ++loads;
-                    const uint32_t to = ring + place * kTileBytes<D> + lane * box * 128, full = bar(bars.full[place]);
-                    const uint32_t bytes = __popc(__ballot_sync(~0u, good)) * box * D * 2;
-                    if (wanted && !good) {   // no such page: the rows that see it become NaN
-                        atomicOr(a.errors, kErrorInput);
-                        for (int x = 0; x < D / 64; ++x)
-                            for (int i = 0; i < box * 128; i += 16)
-                                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(to + x * (kTile * 128) + i),
-                                             "r"(0x7FFF7FFFu)
-                                             : "memory");
-                        writes_before_async();
-                    }
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (bytes) barrier_expect(full, bytes);
-                        else barrier_arrive(full);
-                    }
-                    __syncwarp();
-                    if (good)
-                        for (int x = 0; x < D / 64; ++x)
-                            tile_copy4(to + x * (kTile * 128), map, 64 * x, p & ((1 << a.page_shift) - 1), hk, page, full);
-                    if (ask && lane == 0) barrier_arrive(bar(bars.ask[place]));
-                    __syncwarp();
-                    return true;
-                };
-                const int n = it.n[0];
-                bool ok = load_query(0) && load_ring(&k_map, 0, false) && (it.n[1] == 0 || load_query(1));
-                for (int j = 0; ok && j < n; ++j)
-                    ok = (j == 0 || load_ring(&k_map, j, false)) && load_ring(&v_map, j, j >= it.clean_from);
-                if (!ok) break;
-                c.kt += n - 1, c.pos += n - 1;
-                step<kBlock, kTile, kTilePiece>(a, c);
-                more = c.pos < r.span;
-            }
-        } else {
-            // Sequences are taken 32 at a time, one a lane.  Their items come longest first: by the block's
-            // place in its sequence, falling, then by sequence, then by head.  Every other round of CTAs runs
-            // backwards, which evens out what a CTA gets.
-            int64_t before = 0, chunk = 0;           // items of the chunks before, items of this one
-            int64_t level_before = 0;                // items of the chunk's levels before
-            int base = -32, first = 0, len = 0, blocks = 0, level = 0;
-            uint32_t loads = 0, q_uses[2] = {0, 0};
-            for (uint32_t count = 0;; ++count) {
-                const int64_t want = (int64_t)count * gridDim.x + (count & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-                while (base < a.n && want >= before + chunk) {
-                    before += chunk;
-                    base += 32;
-                    first = len = 0;
-                    if (base + lane < a.n) {
-                        first = min(max(a.cu[base + lane], 0), a.T);
-                        len = min(max(a.cu[base + lane + 1], first), a.T) - first;
-                    }
-                    blocks = (len + kRows - 1) / kRows;
-                    chunk = (int64_t)__reduce_add_sync(~0u, blocks) * a.Hq;
-                    level = __reduce_max_sync(~0u, blocks) - 1;
-                    level_before = 0;
-                }
-                Item it = {};
-                if (base < a.n) {
-                    uint32_t there = __ballot_sync(~0u, blocks > level);
-                    while (want - before >= level_before + (int64_t)__popc(there) * a.Hq) {
-                        level_before += (int64_t)__popc(there) * a.Hq;
-                        there = __ballot_sync(~0u, blocks > --level);
-                    }
-                    const int i = (int)(want - before - level_before);
-                    for (int k = i / a.Hq; k > 0; --k) there &= there - 1;
-                    const int src = __ffs(there) - 1;
-                    it.first = __shfl_sync(~0u, first, src), it.len = __shfl_sync(~0u, len, src);
-                    it.head = i % a.Hq;
-                    it.block = level;
-                    if (kSplit) {
-                        it.n[0] = (level + 2) / 2, it.n[1] = (level + 1) / 2;
-                        it.clean_from = level;
-                    } else {
-                        it.n[0] = 2 * level + 1;
-                        it.n[1] = level * kBlock + kTile < it.len ? 2 * level + 2 : 0;
-                        it.clean_from = 2 * level;
-                    }
-                }
-                const int slot = count % kItems;
-                bool ok = true;
-                if (lane == 0) {
-                    ok = wait(bars.item_free[slot], (count / kItems & 1) ^ 1);
-                    if (ok) {
                         items[slot] = it;
                         barrier_arrive(bar(bars.item_full[slot]));
                     }
-                    if (ok && it.n[0] > 0) {
-                        const int hk = it.head / a.group, n1 = it.n[1], n = max(it.n[0], n1);
-                        auto load_query = [&](int s) {
-                            if (!wait(bars.q_free[s], (q_uses[s] & 1) ^ 1)) return false;
-                            ++q_uses[s];
-                            barrier_expect(bar(bars.q_full[s]), kTileBytes<D>);
-                            for (int c = 0; c < D / 64; ++c)
-                                tile_copy(tiles + s * kTileBytes<D> + c * (kTile * 128), &q_map, 64 * c, it.head,
-                                          it.first + it.block * kRows + s * kTile, bar(bars.q_full[s]));
-                            return true;
-                        };
-                        auto load_ring = [&](const CUtensorMap *map, int tile, bool ask) {
-                            const int place = loads % R;
-                            if (!wait(bars.free_[place], (loads / R & 1) ^ 1)) return false;
-                            ++loads;
-                            barrier_expect(bar(bars.full[place]), kTileBytes<D>);
-                            for (int c = 0; c < D / 64; ++c)
-                                tile_copy(ring + place * kTileBytes<D> + c * (kTile * 128), map, 64 * c, hk,
-                                          it.first + tile * kTile, bar(bars.full[place]));
-                            if (ask) barrier_arrive(bar(bars.ask[place]));
-                            return true;
-                        };
-                        if (kSplit) {   // the keys two tiles ahead of the values
-                            const int all = it.n[0] + n1;
-                            ok = load_query(0) && load_ring(&k_map, 0, false) && (all == 1 || load_ring(&k_map, 1, false));
-                            for (int j = 0; ok && j < all; ++j)
-                                ok = load_ring(&v_map, j, j == all - 1) && (j + 2 >= all || load_ring(&k_map, j + 2, false));
+                    __syncwarp();
+                    if (!more) break;
+                    const int keys = it.len + it.m;
+                    auto load_query = [&](int s) {
+                        if (!warp_wait(bars.q_free[s], (q_uses[s] & 1) ^ 1)) return false;
+                        ++q_uses[s];
+                        if (lane == 0) {
+                            barrier_expect(bar(bars.q_full[s]), a.tile_tokens * a.group * D * 2);
+                            for (int x = 0; x < D / 64; ++x)
+                                tile_copy(tiles + s * kTileBytes<D> + x * (kTile * 128), &q_map, 64 * x, hk * a.group,
+                                          it.first + (2 * it.block + s) * a.tile_tokens, bar(bars.q_full[s]));
+                        }
+                        __syncwarp();
+                        return true;
+                    };
+                    auto load_ring = [&](const CUtensorMap *map, int j, bool ask) {
+                        const int place = loads % R, p = (it.kt0 + j) * kTile + lane * box;
+                        const bool wanted = lane < boxes && p < keys;
+                        const int at = p >> a.page_shift;
+                        const int page = wanted && at < a.table_width ? a.table[(size_t)it.seq * a.ld_table + at] : -1;
+                        const bool good = wanted && page >= 0 && page < a.pages;
+                        if (!warp_wait(bars.free_[place], (loads / R & 1) ^ 1)) return false;
+                        ++loads;
+                        const uint32_t to = ring + place * kTileBytes<D> + lane * box * 128, full = bar(bars.full[place]);
+                        const uint32_t bytes = __popc(__ballot_sync(~0u, good)) * box * D * 2;
+                        if (wanted && !good) {   // no such page: the rows that see it become NaN
+                            atomicOr(a.errors, kErrorInput);
+                            for (int x = 0; x < D / 64; ++x)
+                                for (int i = 0; i < box * 128; i += 16)
+                                    asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(to + x * (kTile * 128) + i),
+                                                 "r"(0x7FFF7FFFu)
+                                                 : "memory");
+                            writes_before_async();
+                        }
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (bytes) barrier_expect(full, bytes);
+                            else barrier_arrive(full);
+                        }
+                        __syncwarp();
+                        if (good)
+                            for (int x = 0; x < D / 64; ++x)
+                                tile_copy4(to + x * (kTile * 128), map, 64 * x, p & ((1 << a.page_shift) - 1), hk, page, full);
+                        if (ask && lane == 0) barrier_arrive(bar(bars.ask[place]));
+                        __syncwarp();
+                        return true;
+                    };
+                    const int n = it.n[0];
+                    bool ok = load_query(0) && load_ring(&k_map, 0, false) && (it.n[1] == 0 || load_query(1));
+                    for (int j = 0; ok && j < n; ++j)
+                        ok = (j == 0 || load_ring(&k_map, j, false)) && load_ring(&v_map, j, j >= it.clean_from);
+                    if (!ok) break;
+                    c.kt += n - 1, c.pos += n - 1;
+                    step<kBlock, kTile, kTilePiece>(a, c);
+                    more = c.pos < r.span;
+                }
+            } else {
+                // Sequences are taken 32 at a time, one a lane.  Their items come longest first: by the block's
+                // place in its sequence, falling, then by sequence, then by head.  Every other round of CTAs runs
+                // backwards, which evens out what a CTA gets.
+                int64_t before = 0, chunk = 0;           // items of the chunks before, items of this one
+                int64_t level_before = 0;                // items of the chunk's levels before
+                int base = -32, first = 0, len = 0, blocks = 0, level = 0;
+                uint32_t loads = 0, q_uses[2] = {0, 0};
+                for (uint32_t count = 0;; ++count) {
+                    const int64_t want = (int64_t)count * gridDim.x + (count & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+                    while (base < a.n && want >= before + chunk) {
+                        before += chunk;
+                        base += 32;
+                        first = len = 0;
+                        if (base + lane < a.n) {
+                            first = min(max(a.cu[base + lane], 0), a.T);
+                            len = min(max(a.cu[base + lane + 1], first), a.T) - first;
+                        }
+                        blocks = (len + kRows - 1) / kRows;
+                        chunk = (int64_t)__reduce_add_sync(~0u, blocks) * a.Hq;
+                        level = __reduce_max_sync(~0u, blocks) - 1;
+                        level_before = 0;
+                    }
+                    Item it = {};
+                    if (base < a.n) {
+                        uint32_t there = __ballot_sync(~0u, blocks > level);
+                        while (want - before >= level_before + (int64_t)__popc(there) * a.Hq) {
+                            level_before += (int64_t)__popc(there) * a.Hq;
+                            there = __ballot_sync(~0u, blocks > --level);
+                        }
+                        const int i = (int)(want - before - level_before);
+                        for (int k = i / a.Hq; k > 0; --k) there &= there - 1;
+                        const int src = __ffs(there) - 1;
+                        it.first = __shfl_sync(~0u, first, src), it.len = __shfl_sync(~0u, len, src);
+                        it.head = i % a.Hq;
+                        it.block = level;
+                        if (kSplit) {
+                            it.n[0] = (level + 2) / 2, it.n[1] = (level + 1) / 2;
+                            it.clean_from = level;
                         } else {
-                            ok = load_query(0) && load_ring(&k_map, 0, false) && (n1 == 0 || load_query(1));
-                            for (int j = 0; ok && j < n; ++j)
-                                ok = (j == 0 || load_ring(&k_map, j, false)) && load_ring(&v_map, j, j >= it.clean_from);
+                            it.n[0] = 2 * level + 1;
+                            it.n[1] = level * kBlock + kTile < it.len ? 2 * level + 2 : 0;
+                            it.clean_from = 2 * level;
                         }
                     }
+                    const int slot = count % kItems;
+                    bool ok = true;
+                    if (lane == 0) {
+                        ok = wait(bars.item_free[slot], (count / kItems & 1) ^ 1);
+                        if (ok) {
+                            items[slot] = it;
+                            barrier_arrive(bar(bars.item_full[slot]));
+                        }
+                        if (ok && it.n[0] > 0) {
+                            const int hk = it.head / a.group, n1 = it.n[1], n = max(it.n[0], n1);
+                            auto load_query = [&](int s) {
+                                if (!wait(bars.q_free[s], (q_uses[s] & 1) ^ 1)) return false;
+                                ++q_uses[s];
+                                barrier_expect(bar(bars.q_full[s]), kTileBytes<D>);
+                                for (int c = 0; c < D / 64; ++c)
+                                    tile_copy(tiles + s * kTileBytes<D> + c * (kTile * 128), &q_map, 64 * c, it.head,
+                                              it.first + it.block * kRows + s * kTile, bar(bars.q_full[s]));
+                                return true;
+                            };
+                            auto load_ring = [&](const CUtensorMap *map, int tile, bool ask) {
+                                const int place = loads % R;
+                                if (!wait(bars.free_[place], (loads / R & 1) ^ 1)) return false;
+                                ++loads;
+                                barrier_expect(bar(bars.full[place]), kTileBytes<D>);
+                                for (int c = 0; c < D / 64; ++c)
+                                    tile_copy(ring + place * kTileBytes<D> + c * (kTile * 128), map, 64 * c, hk,
+                                              it.first + tile * kTile, bar(bars.full[place]));
+                                if (ask) barrier_arrive(bar(bars.ask[place]));
+                                return true;
+                            };
+                            if (kSplit) {   // the keys two tiles ahead of the values
+                                const int all = it.n[0] + n1;
+                                ok = load_query(0) && load_ring(&k_map, 0, false) && (all == 1 || load_ring(&k_map, 1, false));
+                                for (int j = 0; ok && j < all; ++j)
+                                    ok = load_ring(&v_map, j, j == all - 1) && (j + 2 >= all || load_ring(&k_map, j + 2, false));
+                            } else {
+                                ok = load_query(0) && load_ring(&k_map, 0, false) && (n1 == 0 || load_query(1));
+                                for (int j = 0; ok && j < n; ++j)
+                                    ok = (j == 0 || load_ring(&k_map, j, false)) && load_ring(&v_map, j, j >= it.clean_from);
+                            }
+                        }
+                    }
+                    if (!__shfl_sync(~0u, (int)ok, 0) || it.n[0] == 0) break;
                 }
-                if (!__shfl_sync(~0u, (int)ok, 0) || it.n[0] == 0) break;
             }
-        }
-    } else if (warp == 9) {
-        // ---- products ---------------------------------------------------------------
-        give_registers<kFewRegisters>();
-        // The whole warp walks through the waits, so that addresses and control are uniform; one thread issues.
-        constexpr uint32_t kScores = mma_word(kBf16, kTile, kTile, false), kValues = mma_word(kBf16, kTile, D, true);
-        const bool leader = elected();
-        struct Place {
-            uint32_t at, phase;
-            __device__ void next() {
-                if (++at == R) at = 0, phase ^= 1;
-            }
-        };
-        Place place = {0, 0};
-        uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0}, clean_phase = 0;   // clean_phase: a bit a place
-        auto scores = [&](int s, uint32_t at) {
-            const uint32_t q = tile_descriptor(tiles + (kSplit ? 0 : s) * kTileBytes<D>, 16);
-            const uint32_t k = tile_descriptor(ring + at * kTileBytes<D>, 16);
-            if (leader) {
-#pragma unroll
-                for (int x = 0; x < D / 16; ++x) {
-                    const uint32_t step = (x / 4 * (kTile * 128) + x % 4 * 32) / 16;
-                    mma_shared(tmem + s * kTile, q + step, k + step, kScores, x > 0);
+        } else if (warp == 9) {
+            // ---- products ---------------------------------------------------------------
+            // The whole warp walks through the waits, so that addresses and control are uniform; one thread issues.
+            constexpr uint32_t kScores = mma_word(kBf16, kTile, kTile, false), kValues = mma_word(kBf16, kTile, D, true);
+            const bool leader = elected();
+            struct Place {
+                uint32_t at, phase;
+                __device__ void next() {
+                    if (++at == R) at = 0, phase ^= 1;
                 }
-                mma_commit(bar(bars.s_full[s]));
-            }
-        };
-        auto values = [&](int s, uint32_t at, int h, bool add) {   // with one half of the keys
-            const uint32_t v = tile_descriptor(ring + at * kTileBytes<D> + h * (kTile / 2 * 128), kTile * 128);
-            if (leader) {
-#pragma unroll
-                for (int x = 0; x < kTile / 32; ++x)
-                    mma_tensor(tmem + 2 * kTile + s * D, tmem + s * kTile + h * 32 + x * 8, v + x * (2048 / 16), kValues,
-                               add || x > 0);
-            }
-        };
-        auto commit = [&](uint64_t &b) {
-            if (leader) mma_commit(bar(b));
-        };
-        auto run = [&]() {
-            for (uint32_t count = 0;; ++count) {
-                const int slot = count % kItems;
-                if (!warp_wait(bars.item_full[slot], count / kItems & 1)) return;
-                const int n0 = __shfl_sync(~0u, items[slot].n[0], 0), n1 = __shfl_sync(~0u, items[slot].n[1], 0);
-                const int n = max(n0, n1), clean_from = __shfl_sync(~0u, items[slot].clean_from, 0);
-                __syncwarp();
-                if (leader) barrier_arrive(bar(bars.item_free[slot]));
-                if (n0 == 0) return;
-                if constexpr (kSplit) {
-                    const int all = n0 + n1;
-                    if (!warp_wait(bars.q_full[0], q_phase[0])) return;
-                    q_phase[0] ^= 1;
-#pragma unroll
+            };
+            Place place = {0, 0};
+            uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0}, clean_phase = 0;   // clean_phase: a bit a place
+            auto scores = [&](int s, uint32_t at) {
+                const uint32_t q = tile_descriptor(tiles + (kSplit ? 0 : s) * kTileBytes<D>, 16);
+                const uint32_t k = tile_descriptor(ring + at * kTileBytes<D>, 16);
+                if (leader) {
+    #pragma unroll
+                    for (int x = 0; x < D / 16; ++x) {
+                        const uint32_t step = (x / 4 * (kTile * 128) + x % 4 * 32) / 16;
+                        mma_shared(tmem + s * kTile, q + step, k + step, kScores, x > 0);
+                    }
+                    mma_commit(bar(bars.s_full[s]));
+                }
+            };
+            auto values = [&](int s, uint32_t at, int h, bool add) {   // with one half of the keys
+                const uint32_t v = tile_descriptor(ring + at * kTileBytes<D> + h * (kTile / 2 * 128), kTile * 128);
+                if (leader) {
+    #pragma unroll
+                    for (int x = 0; x < kTile / 32; ++x)
+                        mma_tensor(tmem + 2 * kTile + s * D, tmem + s * kTile + h * 32 + x * 8, v + x * (2048 / 16), kValues,
+                                   add || x > 0);
+                }
+            };
+            auto commit = [&](uint64_t &b) {
+                if (leader) mma_commit(bar(b));
+            };
+            auto run = [&]() {
+                for (uint32_t count = 0;; ++count) {
+                    const int slot = count % kItems;
+                    if (!warp_wait(bars.item_full[slot], count / kItems & 1)) return;
+                    const int n0 = __shfl_sync(~0u, items[slot].n[0], 0), n1 = __shfl_sync(~0u, items[slot].n[1], 0);
+                    const int n = max(n0, n1), clean_from = __shfl_sync(~0u, items[slot].clean_from, 0);
+                    __syncwarp();
+                    if (leader) barrier_arrive(bar(bars.item_free[slot]));
+                    if (n0 == 0) return;
+                    if constexpr (kSplit) {
+                        const int all = n0 + n1;
+                        if (!warp_wait(bars.q_full[0], q_phase[0])) return;
+                        q_phase[0] ^= 1;
+    #pragma unroll
+                        for (int s = 0; s < 2; ++s) {
+                            if (s >= all) continue;
+                            if (!warp_wait(bars.full[place.at], place.phase)) return;
+                            tensor_fence_after();
+                            scores(s, place.at);
+                            commit(bars.free_[place.at]);
+                            place.next();
+                        }
+                        if (all <= 2) commit(bars.q_free[0]);
+                        for (int t0 = 0; t0 < all; t0 += 2) {
+    #pragma unroll
+                            for (int s = 0; s < 2; ++s) {
+                                const int t = t0 + s;
+                                if (t >= all) continue;
+                                const bool more = t + 2 < all;
+                                const Place v = place;
+                                place.next();
+                                const Place k = place;   // the keys two tiles on
+                                if (more) place.next();
+                                if (!warp_wait(bars.full[v.at], v.phase)) return;
+                                if (t == all - 1) {
+                                    if (!warp_wait(bars.clean[v.at], clean_phase >> v.at & 1)) return;
+                                    clean_phase ^= 1u << v.at;
+                                }
+                                if (more && !warp_wait(bars.full[k.at], k.phase)) return;
+    #pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    if (!warp_wait(bars.p_full[s][h], p_phase[s])) return;
+                                    tensor_fence_after();
+                                    values(s, v.at, h, t0 > 0 || h > 0);
+                                }
+                                p_phase[s] ^= 1;
+                                if (more) {
+                                    scores(s, k.at);
+                                    if (t + 3 == all) commit(bars.q_free[0]);
+                                } else {
+                                    commit(bars.o_full[s]);
+                                }
+                                commit(bars.free_[v.at]);
+                                if (more) commit(bars.free_[k.at]);
+                            }
+                        }
+                        continue;
+                    }
+                    if (!warp_wait(bars.full[place.at], place.phase)) return;
+    #pragma unroll
                     for (int s = 0; s < 2; ++s) {
-                        if (s >= all) continue;
-                        if (!warp_wait(bars.full[place.at], place.phase)) return;
+                        const int ns = s ? n1 : n0;
+                        if (ns == 0) continue;
+                        if (!warp_wait(bars.q_full[s], q_phase[s])) return;
+                        q_phase[s] ^= 1;
                         tensor_fence_after();
                         scores(s, place.at);
-                        commit(bars.free_[place.at]);
-                        place.next();
+                        if (ns == 1) commit(bars.q_free[s]);
                     }
-                    if (all <= 2) commit(bars.q_free[0]);
-                    for (int t0 = 0; t0 < all; t0 += 2) {
-#pragma unroll
+                    commit(bars.free_[place.at]);
+                    place.next();
+                    for (int j = 0; j < n; ++j) {
+                        const Place v = place;
+                        place.next();
+                        const Place k = place;   // the next keys
+                        if (j + 1 < n) place.next();
+                        if (!warp_wait(bars.full[v.at], v.phase)) return;
+                        if (j >= clean_from) {
+                            if (!warp_wait(bars.clean[v.at], clean_phase >> v.at & 1)) return;
+                            clean_phase ^= 1u << v.at;
+                        }
+                        if (j + 1 < n && !warp_wait(bars.full[k.at], k.phase)) return;
+    #pragma unroll
                         for (int s = 0; s < 2; ++s) {
-                            const int t = t0 + s;
-                            if (t >= all) continue;
-                            const bool more = t + 2 < all;
-                            const Place v = place;
-                            place.next();
-                            const Place k = place;   // the keys two tiles on
-                            if (more) place.next();
-                            if (!warp_wait(bars.full[v.at], v.phase)) return;
-                            if (t == all - 1) {
-                                if (!warp_wait(bars.clean[v.at], clean_phase >> v.at & 1)) return;
-                                clean_phase ^= 1u << v.at;
-                            }
-                            if (more && !warp_wait(bars.full[k.at], k.phase)) return;
-#pragma unroll
+                            const int ns = s ? n1 : n0;
+                            if (j >= ns) continue;
+    #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 if (!warp_wait(bars.p_full[s][h], p_phase[s])) return;
                                 tensor_fence_after();
-                                values(s, v.at, h, t0 > 0 || h > 0);
+                                values(s, v.at, h, j > 0 || h > 0);
                             }
                             p_phase[s] ^= 1;
-                            if (more) {
-                                scores(s, k.at);
-                                if (t + 3 == all) commit(bars.q_free[0]);
-                            } else {
+                            if (j + 1 == ns) {
                                 commit(bars.o_full[s]);
+                            } else {
+                                scores(s, k.at);
+                                if (j + 2 == ns) commit(bars.q_free[s]);
                             }
-                            commit(bars.free_[v.at]);
-                            if (more) commit(bars.free_[k.at]);
                         }
+                        commit(bars.free_[v.at]);
+                        if (j + 1 < n) commit(bars.free_[k.at]);
                     }
-                    continue;
                 }
-                if (!warp_wait(bars.full[place.at], place.phase)) return;
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const int ns = s ? n1 : n0;
-                    if (ns == 0) continue;
-                    if (!warp_wait(bars.q_full[s], q_phase[s])) return;
-                    q_phase[s] ^= 1;
-                    tensor_fence_after();
-                    scores(s, place.at);
-                    if (ns == 1) commit(bars.q_free[s]);
-                }
-                commit(bars.free_[place.at]);
-                place.next();
-                for (int j = 0; j < n; ++j) {
-                    const Place v = place;
-                    place.next();
-                    const Place k = place;   // the next keys
-                    if (j + 1 < n) place.next();
-                    if (!warp_wait(bars.full[v.at], v.phase)) return;
-                    if (j >= clean_from) {
-                        if (!warp_wait(bars.clean[v.at], clean_phase >> v.at & 1)) return;
-                        clean_phase ^= 1u << v.at;
-                    }
-                    if (j + 1 < n && !warp_wait(bars.full[k.at], k.phase)) return;
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        const int ns = s ? n1 : n0;
-                        if (j >= ns) continue;
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (!warp_wait(bars.p_full[s][h], p_phase[s])) return;
-                            tensor_fence_after();
-                            values(s, v.at, h, j > 0 || h > 0);
-                        }
-                        p_phase[s] ^= 1;
-                        if (j + 1 == ns) {
-                            commit(bars.o_full[s]);
-                        } else {
-                            scores(s, k.at);
-                            if (j + 2 == ns) commit(bars.q_free[s]);
-                        }
-                    }
-                    commit(bars.free_[v.at]);
-                    if (j + 1 < n) commit(bars.free_[k.at]);
-                }
-            }
-        };
-        run();
-        commit(bars.done);   // no arrival of a commit is under way when the CTA's memory goes
-        warp_wait(bars.done, 0);
-    } else if (warp >= 10) {
-        // ---- values that are not finite, in the tiles on the diagonal ------------------
-        give_registers<kFewRegisters>();
-        uint32_t loads = 0, asks = 0;
-        bool ok = true;
-        for (uint32_t count = 0; ok; ++count) {
-            const int slot = count % kItems;
-            ok = warp_wait(bars.item_full[slot], count / kItems & 1);
-            if (!ok) break;
-            const int n0 = items[slot].n[0], n1 = items[slot].n[1], n = kSplit ? n0 + n1 : max(n0, n1);
-            const int from = items[slot].clean_from;
-            // keys of the tile, counted from the first tile looked at
-            const int keys = items[slot].len + items[slot].m - (kCache ? items[slot].len / kTile : from) * kTile;
-            const int skip = kCache ? items[slot].kt0 + from - items[slot].len / kTile : 0;
-            for (int j = from; ok && j < n; ++j) {
-                const uint32_t i = loads + 2 * j + 1;
-                const int place = i % R;
-                ok = warp_wait(bars.ask[place], asks >> place & 1) && warp_wait(bars.full[place], i / R & 1);
+            };
+            run();
+            commit(bars.done);   // no arrival of a commit is under way when the CTA's memory goes
+            warp_wait(bars.done, 0);
+        } else {
+            // ---- values that are not finite, in the tiles on the diagonal ------------------
+            uint32_t loads = 0, asks = 0;
+            bool ok = true;
+            for (uint32_t count = 0; ok; ++count) {
+                const int slot = count % kItems;
+                ok = warp_wait(bars.item_full[slot], count / kItems & 1);
                 if (!ok) break;
-                asks ^= 1u << place;
-                const uint32_t at = ring + place * kTileBytes<D>;
-#pragma unroll 4
-                for (int c = tid - 320; c < kTileBytes<D> / 16; c += 64) {
-                    uint32_t w[4];
-                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                                 : "r"(at + c * 16)
-                                 : "memory");
-                    // a half whose magnitude reaches the exponent of infinity carries into its sign bit
-                    constexpr uint32_t kStep = kBf16 ? 0x00800080u : 0x04000400u;
-                    uint32_t odd = 0;
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) odd |= (w[x] & 0x7FFF7FFFu) + kStep;
-                    if (odd & 0x80008000u) {
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + c * 16), "r"(finite_part<E>(w[0])),
-                                     "r"(finite_part<E>(w[1])), "r"(finite_part<E>(w[2])), "r"(finite_part<E>(w[3]))
+                const int n0 = items[slot].n[0], n1 = items[slot].n[1], n = kSplit ? n0 + n1 : max(n0, n1);
+                const int from = items[slot].clean_from;
+                // keys of the tile, counted from the first tile looked at
+                const int keys = items[slot].len + items[slot].m - (kCache ? items[slot].len / kTile : from) * kTile;
+                const int skip = kCache ? items[slot].kt0 + from - items[slot].len / kTile : 0;
+                for (int j = from; ok && j < n; ++j) {
+                    const uint32_t i = loads + 2 * j + 1;
+                    const int place = i % R;
+                    ok = warp_wait(bars.ask[place], asks >> place & 1) && warp_wait(bars.full[place], i / R & 1);
+                    if (!ok) break;
+                    asks ^= 1u << place;
+                    const uint32_t at = ring + place * kTileBytes<D>;
+    #pragma unroll 4
+                    for (int c = tid - 320; c < kTileBytes<D> / 16; c += 64) {
+                        uint32_t w[4];
+                        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                     : "r"(at + c * 16)
                                      : "memory");
-                        const int row = c / 8 % kTile;
-                        const int tile = j - from + skip;   // 0 or 1
-                        if (tile * kTile + row < keys) atomicOr(&items[slot].odd[tile][row / 32], 1u << row % 32);
+                        // a half whose magnitude reaches the exponent of infinity carries into its sign bit
+                        constexpr uint32_t kStep = kBf16 ? 0x00800080u : 0x04000400u;
+                        uint32_t odd = 0;
+    #pragma unroll
+                        for (int x = 0; x < 4; ++x) odd |= (w[x] & 0x7FFF7FFFu) + kStep;
+                        if (odd & 0x80008000u) {
+                            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + c * 16), "r"(finite_part<E>(w[0])),
+                                         "r"(finite_part<E>(w[1])), "r"(finite_part<E>(w[2])), "r"(finite_part<E>(w[3]))
+                                         : "memory");
+                            const int row = c / 8 % kTile;
+                            const int tile = j - from + skip;   // 0 or 1
+                            if (tile * kTile + row < keys) atomicOr(&items[slot].odd[tile][row / 32], 1u << row % 32);
+                        }
                     }
+                    writes_before_async();
+                    __syncwarp();
+                    if (lane == 0) barrier_arrive(bar(bars.clean[place]));
                 }
-                writes_before_async();
+                loads += 2 * n;
                 __syncwarp();
-                if (lane == 0) barrier_arrive(bar(bars.clean[place]));
+                if (lane == 0) barrier_arrive(bar(bars.item_free[slot]));
+                if (n0 == 0) break;
             }
-            loads += 2 * n;
-            __syncwarp();
-            if (lane == 0) barrier_arrive(bar(bars.item_free[slot]));
-            if (n0 == 0) break;
         }
     } else {
         // ---- softmax and output: one row a thread ----------------------------------------

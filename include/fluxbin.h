@@ -362,7 +362,10 @@ FB_API fb_status fb_qk_norm_rope(const fb_heads *in, const fb_heads *out, const 
  * Rows of no sequence keep their contents.  What lies outside a sequence, and
  * later tokens within it, never reaches a row, whatever the values (NaN and
  * infinity included).  The weights p are rounded to in->t before they meet v
- * (the tensor cores take operands of one type), their sum is of fp32 values.
+ * (the tensor cores take operands of one type), their sum is of fp32 values:
+ * by at most 2^-8 (bf16) or 2^-11 (fp16) of their size, and as fp16 has few
+ * exponents, there also by 2^-32 of the row's largest (weights below 2^-21 of
+ * it lose bits, those below 2^-32 may be dropped).
  * An infinite or NaN score among those a row sees makes the row NaN. */
 FB_API fb_status fb_attn_prompt(const fb_heads *in, const int32_t *cu_seqlens, int n, float scale, void *out, int ldo,
                                 float *lse, unsigned flags, void *stream);
@@ -387,9 +390,10 @@ FB_API fb_status fb_attn_prompt(const fb_heads *in, const int32_t *cu_seqlens, i
  * more than max_draft tokens leaves those behind them unwritten; both raise
  * bit 0 of fb_attn_errors, and no memory outside the cache is read.  Tokens
  * of no sequence keep their contents.  Where a key head has at most 16 rows
- * (max_draft * Hq / Hkv) the weights keep 2^-16 of their size, and an infinite
- * value among the committed keys gives infinity or NaN; with more rows they
- * are rounded as in fb_attn_prompt.
+ * (max_draft * Hq / Hkv) the weights are off by at most 2^-16 of their size
+ * (fp16: and 2^-32 of the row's largest), with more rows they are rounded as in
+ * fb_attn_prompt.  An infinite value among the committed keys gives infinity or
+ * NaN.
  * ws: fb_attn_tree_workspace_bytes bytes, 16-byte aligned, for the partial
  * results of sequences split over several CTAs; its contents need not be
  * set up and mean nothing afterwards, but calls that may run at the same

@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "fb_internal.cuh"
 
 namespace fb {
@@ -15,9 +17,16 @@ constexpr int kMaxTokens = 1 << 24;
 constexpr int kMaxHeads = 1024;
 
 // Outputs are rescaled only when a row's maximum has grown by more than 2^8 since
-// the last time: the sum carries the same factor, and weights up to 2^8 lose
-// nothing in either type.
+// the last time: the sum carries the same factor, and weights that much larger
+// fit either type.
 constexpr float kRescaleLog2 = 8.0f;
+// What a row's weights are relative to lies this many powers of two below its
+// maximum: fp16 holds weights from 2^-14 in full and drops them below 2^-25, so
+// its largest stands at 2^7, and at no more than 2^15 after a growth that asks
+// for no rescaling.  The sum, its logarithm and the joins carry the factor.
+// bf16 has fp32's range and needs none.
+template <typename E>
+constexpr float kHeadroomLog2 = std::is_same_v<E, __half> ? 7.0f : 0.0f;
 
 // Device address of the word in which the attention kernels raise the bits of
 // fb_attn_errors, on the current device (null on a CUDA error).

@@ -37,7 +37,7 @@
 //
 // The outputs are rescaled only when a row's maximum has grown by more than
 // 2^8 since the last time (exact all the same: the sum carries the same factor,
-// and weights up to 2^8 lose nothing in either type), which few tiles need.
+// and weights that much larger fit either type), which few tiles need.
 #pragma once
 
 #include <cuda.h>
@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             } else {
                 row = items[slot].block * kRows + (kSplit ? 0 : s * kTile) + local;
             }
-            float m = -INFINITY, l = 0.0f;   // m: the (scaled) maximum that the weights so far are relative to
+            float m = -INFINITY, l = 0.0f;   // m: what the weights so far are relative to, from a (scaled) maximum
             for (int j = 0; j < n; ++j) {
                 ok = warp_wait(bars.s_full[s], s_uses++ & 1);
                 if (!ok) break;
@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         top[c] = max3(top[c], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
                     top[c] = max3(top[c], __uint_as_float(x[c][31]), __uint_as_float(x[c][31]));
                 }
-                const float mn = max3(max3(top[0], top[1], top[2]), top[3], top[3]) * a.scale_log2;
+                const float mn = max3(max3(top[0], top[1], top[2]), top[3], top[3]) * a.scale_log2 - kHeadroomLog2<E>;
                 if (!(mn < INFINITY)) l = NAN;   // a score that is NaN or infinite: the row has no weights
                 const bool grown = mn > m + kRescaleLog2;   // also the first finite score of the row
                 if (__any_sync(~0u, grown)) {

@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
 
         float o[MT][D / 8][4] = {};
-        float m[MT][2], l[MT][2];   // m: the (scaled) maximum that the weights so far are relative to
+        float m[MT][2], l[MT][2];   // m: what the weights so far are relative to, from a (scaled) maximum
 #pragma unroll
         for (int t = 0; t < MT; ++t) m[t][0] = m[t][1] = -INFINITY, l[t][0] = l[t][1] = 0.0f;
 
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             }
 
             // The outputs are rescaled only when a row's maximum has grown by more than 2^8 since the last time:
-            // the sum carries the same factor, and weights up to 2^8 lose nothing in either type.
+            // the sum carries the same factor, and weights that much larger fit either type.
             float top[MT][2];
             bool grown = false;
 #pragma unroll
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     for (int j = 0; j < NT; ++j) x = fmaxf(x, fmaxf(s[t][j][2 * half], s[t][j][2 * half + 1]));
                     x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
                     x = fmaxf(x, __shfl_xor_sync(~0u, x, 2));
-                    top[t][half] = x * a.scale_log2;
+                    top[t][half] = x * a.scale_log2 - kHeadroomLog2<E>;
                     grown |= top[t][half] > m[t][half] + kRescaleLog2;   // also the first finite score of a row
                 }
             if (__any_sync(~0u, grown)) {
@@ -373,7 +373,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             }
             // For up to 16 rows the weights meet the values as two operands, the rounded weight and what the rounding
             // left: beside the stream of keys the second product costs nothing there, and the weights lose no more
-            // than 2^-16 of their size.  For more rows it would cost 12%; there they are rounded once.
+            // than 2^-16 of their size (fp16: or 2^-32 of the largest).  For more rows it would cost 12%; there they
+            // are rounded once.
             uint32_t pa[MT][NT / 2][4], pr[MT][NT / 2][4];
 #pragma unroll
             for (int t = 0; t < MT; ++t)

@@ -362,6 +362,43 @@ def test_prompt_side_stream_and_graph():
     assert torch.equal(out, fb.fb_attn_prompt(q, k, v, cud))
 
 
+# Every 16th key is a sink: it outscores the others by 2^octaves and its value is zero, so the output is made of the
+# others' small weights.  The bound is of each weight: `w` of its size, and for fp16 half a step of its subnormals,
+# 2^-25, against a largest weight of at least 2^7: 2^-32 of a sink's.
+
+
+SINKS = [3.0, 18.3, 20.6, 22.4, 24.6, 25.5]
+
+
+def check_sinks(out, refs, octaves, most, D, dtype, w, what):
+    for rows, head, (ro, rl, wabs, sabs), n in refs:
+        e_p = 2 * sabs * (D + 2) * U + 2.0 ** -18
+        floor = 2.0 ** -32 * n * most * np.exp(octaves * np.log(2) - rl) if dtype == torch.float16 else 0 * rl
+        bound = HALF[dtype] * np.abs(ro) + (w + 2 * e_p + (n + 64) * U)[:, None] * wabs + floor[:, None] + TINY[dtype]
+        assert_within(f64(out)[rows, head], ro, bound, f"{what}: head {head}")
+
+
+def sinks_in(k, v, octaves, g):
+    """k, v [keys, heads, D]: scores 0 but for every 16th key, for queries that are the first unit vector."""
+    k.zero_()
+    k[::16, :, 0] = octaves * np.log(2)
+    v.copy_(256 * (1 + torch.rand(v.shape, generator=g, device=DEV)))
+    v[::16] = 0
+    return float(k[0, 0, 0]) / np.log(2)
+
+
+@pytest.mark.parametrize("octaves", SINKS)
+@pytest.mark.parametrize("H", [2, 320])
+@pytest.mark.parametrize("D,dtype", [(64, torch.float16), (128, torch.float16), (64, torch.bfloat16)])
+def test_prompt_small_weights_beside_sinks(D, dtype, H, octaves):
+    n = 700
+    q, k, v = (torch.zeros(n, h, D, dtype=dtype, device=DEV) for h in (H, 1, 1))
+    q[..., 0] = 1
+    octaves = sinks_in(k, v, octaves, gen(51))
+    out = fb.fb_attn_prompt(q, k, v, torch.tensor([0, n], dtype=torch.int32, device=DEV), 1.0)
+    check_sinks(out, prompt_refs(q, k, v, [0, n], 1.0, heads=[H - 1]), octaves, 512, D, dtype, HALF[dtype], "prompt")
+
+
 # ---- trees over a paged cache ----------------------------------------------------
 
 
@@ -462,6 +499,27 @@ def test_tree(case, chain):
     o2, l2 = tree_call(c, masks, scale, flags=fb.FB_GEMV_PDL)
     assert torch.equal(out, o2) and torch.equal(lse, l2)
     assert fb.fb_attn_errors() == 0
+
+
+# up to 16 rows a key head (weights good to 2^-16), up to 32, more by each path
+@pytest.mark.parametrize("octaves", SINKS)
+@pytest.mark.parametrize("Hq,drafts,page_size,dtype", [
+    (1, 12, 16, torch.float16), (2, 7, 4, torch.float16), (1, 16, 64, torch.bfloat16), (4, 8, 64, torch.float16),
+    (4, 20, 4, torch.float16), (8, 20, 16, torch.float16)])
+def test_tree_small_weights_beside_sinks(Hq, drafts, page_size, dtype, octaves):
+    D = 64
+    c = tree_inputs([1600, 30], [drafts, 1], Hq, 1, D, page_size, dtype, seed=52)
+    c["q"].zero_()
+    c["q"][..., 0] = 1
+    for s, (a, m) in enumerate(zip(c["lens"], c["drafts"])):
+        p = np.arange(a + m)
+        k, v = (torch.empty(a + m, 1, D, dtype=dtype, device=DEV) for _ in range(2))
+        octaves = sinks_in(k, v, octaves, gen(53 + s))
+        pages, rows = torch.tensor(c["table"][s][p // page_size], device=DEV).long(), torch.tensor(p % page_size, device=DEV)
+        c["k"][pages, 0, rows], c["v"][pages, 0, rows] = k[:, 0], v[:, 0]
+    out, _ = tree_call(c, None, 1.0)
+    check_sinks(out, tree_refs(c, None, 1.0, heads=[Hq - 1]), octaves, 512, D, dtype,
+                2.0 ** -16 if Hq * drafts <= 16 else HALF[dtype], "tree")
 
 
 def test_tree_single_tokens_without_offsets():

@@ -338,9 +338,10 @@ typedef struct fb_kv_cache {
  *   being elements (p, p + rot/2), or with FB_ROPE_NEIGHBOURS (2p, 2p + 1);
  *   values are only converted.
  * in->t: any type; out->t: FB_F16 or FB_BF16, the same T, Hq, Hkv, D.  Each of
- * out->q, out->k, out->v may be NULL (not written) or the input itself when
- * type and pitch agree (in place); otherwise they must not overlap the
- * inputs.  cache (may be NULL; type out->t) takes token i's keys and values
+ * out->q, out->k, out->v may be NULL (not written) or its own input when type
+ * and pitch agree (in place); otherwise outputs overlap neither inputs nor each
+ * other (FB_ERR_INVALID_VALUE; rows of one pitch may lie between each other's,
+ * rows of different pitches not).  cache (may be NULL; type out->t) takes token i's keys and values
  * at slot slots[i]; a slot outside [0, pages*page_size) is skipped, and the
  * same slot twice leaves either token's elements.  pos: T int32, any sign;
  * inv_freq: rot/2 doubles (8-byte aligned); angles are reduced in fp64, so a

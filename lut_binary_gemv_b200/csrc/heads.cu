@@ -193,6 +193,36 @@ cudaError_t launch_rotate(const RotateArgs &a, int T, bool pdl, cudaStream_t s) 
     }
 }
 
+// T rows of `width` bytes, `pitch` bytes apart.
+struct Rows {
+    const void *at;
+    int64_t pitch, width;
+};
+inline int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b != 0 && a < 0); }
+// Whether two sets of rows share a byte: exactly where the pitches agree (slices of one buffer lie between each
+// other's rows), else by what they span.
+bool overlap(const Rows &a, const Rows &b, int64_t T) {
+    if (!a.at || !b.at) return false;
+    const int64_t d = (int64_t)((uintptr_t)b.at - (uintptr_t)a.at), last = T - 1;
+    if (T == 1 || a.pitch != b.pitch) return d < last * a.pitch + a.width && -d < last * b.pitch + b.width;
+    // row i of a meets row i + k of b where -b.width < d + k * pitch < a.width
+    const int64_t k0 = floor_div(-b.width - d, a.pitch) + 1, k1 = -floor_div(d - a.width, a.pitch) - 1;
+    return k0 <= k1 && k0 <= last && k1 >= -last;
+}
+
+// An output may be its own input, row for row, and meets no other input or output.
+bool outputs_apart(const fb_heads &in, const fb_heads &out) {
+    const int64_t ei = dtype_size(in.t), eo = dtype_size(out.t), wq = (int64_t)in.Hq * in.D, wk = (int64_t)in.Hkv * in.D;
+    const Rows i[3] = {{in.q, in.ldq * ei, wq * ei}, {in.k, in.ldk * ei, wk * ei}, {in.v, in.ldv * ei, wk * ei}};
+    const Rows o[3] = {{out.q, out.ldq * eo, wq * eo}, {out.k, out.ldk * eo, wk * eo}, {out.v, out.ldv * eo, wk * eo}};
+    for (int x = 0; x < 3; ++x)
+        for (int y = 0; y < 3; ++y) {
+            const bool same = x == y && o[x].at == i[y].at && in.t == out.t && (o[x].pitch == i[y].pitch || in.T == 1);
+            if ((!same && overlap(o[x], i[y], in.T)) || (y > x && overlap(o[x], o[y], in.T))) return false;
+        }
+    return true;
+}
+
 template <typename TO>
 cudaError_t launch_rotate_to(fb_dtype t, const RotateArgs &a, int T, bool pdl, cudaStream_t s) {
     if (t == FB_F32) return launch_rotate<float, TO>(a, T, pdl, s);
@@ -229,6 +259,7 @@ extern "C" fb_status fb_qk_norm_rope(const fb_heads *in, const fb_heads *out, co
         !aligned(q_weight, 4) || !aligned(k_weight, 4) || !aligned(slots, 4) ||
         (cache && (!aligned(cache->k, 16) || !aligned(cache->v, 16))))
         return FB_ERR_MISALIGNED;
+    if (!outputs_apart(*in, *out)) return FB_ERR_INVALID_VALUE;
     RotateArgs a = {};
     a.q = in->q, a.k = in->k, a.v = in->v;
     a.qo = out->q, a.ko = out->k, a.vo = out->v;

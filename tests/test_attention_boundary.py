@@ -70,6 +70,32 @@ def test_rope_refusals(L, args, status):
     assert rope(L, **args) == status
 
 
+# in: q at 1 MB, k at 2 MB, v at 3 MB; rows of 2048, 512 and 512 bytes (bf16)
+MB = 1 << 20
+
+
+@pytest.mark.parametrize("args", [
+    dict(hout=heads(q=MB, k=None, v=None, ldq=1032)),                       # in place with another pitch
+    dict(hout=heads(q=MB, k=None, v=None, t=F16), cache=kv_cache(t=F16)),   # ... with another type
+    dict(hin=heads(q=MB, k=2 * MB, v=3 * MB, t=F32), hout=heads(q=MB, k=None, v=None)),
+    dict(hout=heads(q=None, k=None, v=2 * MB)),                             # an output that is another input
+    dict(hout=heads(q=2 * MB, k=None, v=None)),
+    dict(hin=heads(q=MB, k=2 * MB, v=2 * MB), hout=heads(q=None, k=2 * MB, v=None)),   # keys that are the values too
+    dict(hout=heads(q=MB + 16, k=None, v=None)),                            # a part of its input
+    dict(hout=heads(q=MB - 2048 * 4 + 16, k=None, v=None)),
+    dict(hout=heads(q=MB + 2048 * 3 + 2032, k=None, v=None)),
+    dict(hout=heads(q=None, k=2 * MB + 512, v=None)),                       # its input one row on
+    dict(hout=heads(q=None, k=8 * MB, v=8 * MB)),                           # two outputs in one place
+    dict(hout=heads(q=8 * MB, k=8 * MB + 2048 * 3, v=None)),
+    dict(hin=heads(q=MB, k=MB + 2048, v=MB + 2560, ldq=1536, ldk=1536, ldv=1536),     # slices of one projection
+         hout=heads(q=MB + 16, k=None, v=None, ldq=1536)),
+    dict(hin=heads(q=MB, k=MB + 2048, v=MB + 2560, ldq=1536, ldk=1536, ldv=1536),
+         hout=heads(q=None, k=MB + 2560, v=None, ldk=1536)),
+])
+def test_rope_refuses_outputs_that_overlap(L, args):
+    assert rope(L, **{"hin": heads(q=MB, k=2 * MB, v=3 * MB), **args}) == INVALID
+
+
 OUT = 0x20000
 
 

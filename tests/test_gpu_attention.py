@@ -147,6 +147,27 @@ def test_rope_in_place_and_beside_the_cache():
     assert torch.equal(rows[slots.long()], kr)
 
 
+def test_rope_outputs_between_the_rows_of_the_inputs():
+    # q, k, v and all outputs in one buffer: rows side by side, and in place beside strangers
+    q, k, v, pos, freq, wq, wk, *_ = rope_case(37, 4, 2, 64, 64, True, False, torch.bfloat16, torch.bfloat16, 0, seed=10)
+    want = fb.fb_qk_norm_rope(q, k, v, pos, freq, wq, wk)
+    buf = torch.full((37, 18, 64), 3.0, dtype=torch.bfloat16, device=DEV)
+    buf[:, 1:9] = torch.cat([q, k, v], 1)
+    parts = lambda at: (buf[:, at:at + 4], buf[:, at + 4:at + 6], buf[:, at + 6:at + 8])  # noqa: E731
+    got = fb.fb_qk_norm_rope(*parts(1), pos, freq, wq, wk, q_out=parts(9)[0], k_out=parts(9)[1], v_out=parts(9)[2])
+    assert all(torch.equal(g, w) for g, w in zip(got, want)) and torch.equal(buf[:, 1:9], torch.cat([q, k, v], 1))
+    assert bool((buf[:, [0, 17]] == 3.0).all())
+    got = fb.fb_qk_norm_rope(*parts(1), pos, freq, wq, wk, q_out=parts(1)[0], k_out=parts(1)[1], v_out=parts(1)[2])
+    assert all(torch.equal(g, w) for g, w in zip(got, want)) and bool((buf[:, [0, 17]] == 3.0).all())
+    one = q[:1].clone()
+    fb.fb_qk_norm_rope(one, k[:1], v[:1], pos[:1], freq, wq, wk, q_out=one)
+    assert torch.equal(one, want[0][:1])
+    wide = torch.zeros(37, 5, 64, dtype=torch.bfloat16, device=DEV)
+    wide[:, :4] = q
+    with pytest.raises(fb.FbError, match="INVALID_VALUE"):   # rows of another pitch over the input's
+        fb.fb_qk_norm_rope(wide[:, :4], k, v, pos, freq, wq, wk, q_out=wide.view(-1)[:37 * 256].view(37, 4, 64))
+
+
 def test_rope_skips_slots_outside_the_cache():
     q, k, v, pos, freq, wq, wk, cache, slots = rope_case(9, 4, 2, 64, 64, True, False, torch.float16, torch.float16,
                                                          4, seed=5)

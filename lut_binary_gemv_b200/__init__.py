@@ -449,6 +449,13 @@ def _on(device: int, f, *args) -> int:
     return f(*args, torch.cuda.current_stream(device).cuda_stream if _raw_stream is None else _raw_stream(device))
 
 
+def _pitch(ld: int, what: str) -> int:
+    """A pitch as the C ABI takes it: ctypes would cut a longer one off."""
+    if ld >= 1 << 31:
+        raise ValueError(f"{what}: rows at most 2^31 - 1 elements apart are expected, got {ld}")
+    return ld
+
+
 def _rows(t: torch.Tensor, what: str, device: int, shape, dtype) -> int:
     """The row pitch of [T, H, D] heads on the GPU whose heads are contiguous within a row."""
     if t.dtype == dtype and t.shape == shape and t.get_device() == device >= 0:
@@ -457,7 +464,7 @@ def _rows(t: torch.Tensor, what: str, device: int, shape, dtype) -> int:
             return H * D
         st = t.stride()
         if (st[2] == 1 or D == 1) and (st[1] == D or H == 1):
-            return st[0] if T > 1 else H * D
+            return _pitch(st[0], what) if T > 1 else H * D
         raise ValueError(f"{what}: the heads of a row must be contiguous (only rows may be strided)")
     raise ValueError(f"{what}: a {dtype} tensor {tuple(shape)} on the GPU of the others is expected, "
                      f"got {t.dtype} {tuple(t.shape)} on {t.device}")
@@ -604,7 +611,7 @@ def fb_attn_tree(q: torch.Tensor, cache, page_table: torch.Tensor, lens: torch.T
         ld, unit = page_table.stride()
         if (unit != 1 and width > 1) or (ld < width and n > 1):
             raise ValueError("page_table: unit column stride")
-        ld = ld if n > 1 else width
+        ld = _pitch(ld, "page_table") if n > 1 else width
     if out is None:
         out = torch.empty(qs, dtype=dtype, device=q.device)
     if ws is None:

@@ -193,6 +193,96 @@ def test_binding_refuses_what_is_not_on_the_gpu_or_shaped_otherwise():
         fb.fb_attn_tree(q, (k, k), cu[None], cu)
 
 
+class Sketch:
+    """What the binding asks of a tensor on GPU 0, without the memory."""
+
+    def __init__(self, shape, dtype, strides=None, device=0):
+        self.shape, self.dtype, self._device = torch.Size(shape), dtype, device
+        full = [math.prod(shape[i + 1:]) for i in range(len(shape))]
+        self._strides = tuple(strides or full)
+        self._plain = list(self._strides) == full
+        self.device = torch.device("cuda", device)
+
+    def get_device(self):
+        return self._device
+
+    def is_contiguous(self):
+        return self._plain
+
+    def stride(self):
+        return self._strides
+
+    def numel(self):
+        return math.prod(self.shape)
+
+    def element_size(self):
+        return 2
+
+    def data_ptr(self):
+        return FAKE
+
+
+class Recorder:
+    """In the library's place: notes what reaches it, and on which device."""
+
+    def __init__(self, current, sizes=None):
+        self.calls, self._current, self._sizes = [], current, sizes or {}
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, self._current[0], args))
+            return self._sizes.get(name, 0)
+        return call
+
+
+@pytest.fixture
+def sketched(monkeypatch):
+    current = [0]
+    recorder = Recorder(current)
+
+    class Device:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.device
+
+        def __exit__(self, *_):
+            current[0] = self.before
+
+    monkeypatch.setattr(fb, "lib", lambda: recorder)
+    monkeypatch.setattr(fb, "_get_device", lambda: current[0])
+    monkeypatch.setattr(fb, "_raw_stream", lambda device: 0)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: type("S", (), {"cuda_stream": 0}))
+    monkeypatch.setattr(torch, "empty", lambda shape, dtype, device: Sketch([shape] if isinstance(shape, int) else shape, dtype))
+    recorder.current = current
+    return recorder
+
+
+@pytest.mark.parametrize("far", [2 ** 31, 2 ** 32 + 512])
+def test_binding_refuses_pitches_past_32_bits(sketched, far):
+    # the C ABI's pitches are ints: cut off, 2^32 + 512 would have passed for 512
+    bf = torch.bfloat16
+    h = lambda H, pitch=None: Sketch((2, H, 64), bf, pitch and (pitch, 64, 1))  # noqa: E731
+    i32 = lambda *shape: Sketch(shape, torch.int32)  # noqa: E731
+    q, kv, cu = h(8), h(2), i32(2)
+    cache = (Sketch((4, 2, 16, 64), bf), Sketch((4, 2, 16, 64), bf))
+    table, wide = i32(2, 4), Sketch((2, 4), torch.int32, (far, 1))
+    for call in (lambda: fb.fb_attn_prompt(h(8, far), kv, kv, cu), lambda: fb.fb_attn_prompt(q, kv, h(2, far), cu),
+                 lambda: fb.fb_attn_prompt(q, kv, kv, cu, out=h(8, far)),
+                 lambda: fb.fb_attn_tree(h(8, far), cache, table, i32(2)),
+                 lambda: fb.fb_attn_tree(q, cache, table, i32(2), out=h(8, far)),
+                 lambda: fb.fb_attn_tree(q, cache, wide, i32(2)),
+                 lambda: fb.fb_qk_norm_rope(q, h(2, far), kv, None, None),
+                 lambda: fb.fb_qk_norm_rope(q, kv, kv, None, None, q_out=h(8, far))):
+        with pytest.raises(ValueError):
+            call()
+    assert not [c for c in sketched.calls if not c[0].endswith("_bytes")]
+    fb.fb_attn_tree(h(8, 2 ** 31 - 8), cache, Sketch((2, 4), torch.int32, (2 ** 31 - 1, 1)), i32(2))
+    assert sketched.calls[-1][0] == "fb_attn_tree" and sketched.calls[-1][2][1] == 2 ** 31 - 8
+
+
 def test_rope_frequencies():
     f = fb.rope_frequencies(8, 10000.0, device="cpu")
     assert f.dtype == torch.float64 and torch.allclose(f, torch.tensor([1.0, 0.1, 0.01, 0.001], dtype=torch.float64),

@@ -580,8 +580,16 @@ def fb_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens
 
 def fb_attn_tree_workspace_bytes(Hq: int, cache, max_draft: int, table_width: int) -> int:
     """Bytes of the workspace that fb_attn_tree needs (0: none) for Hq query heads over the cache."""
-    return lib().fb_attn_tree_workspace_bytes(Hq, _cache_bytes(cache, cache[0].get_device(), cache[0].dtype)[0],
-                                              max_draft, table_width)
+    dev = cache[0].get_device()
+    return _tree_workspace(dev, Hq, _cache_bytes(cache, dev, cache[0].dtype)[0], max_draft, table_width)
+
+
+def _tree_workspace(device: int, *args) -> int:
+    """The size goes by the SMs of the device that runs the call, whichever is current."""
+    if device < 0 or device == _get_device():
+        return lib().fb_attn_tree_workspace_bytes(*args)
+    with torch.cuda.device(device):
+        return lib().fb_attn_tree_workspace_bytes(*args)
 
 
 def fb_attn_tree(q: torch.Tensor, cache, page_table: torch.Tensor, lens: torch.Tensor,
@@ -615,7 +623,7 @@ def fb_attn_tree(q: torch.Tensor, cache, page_table: torch.Tensor, lens: torch.T
     if out is None:
         out = torch.empty(qs, dtype=dtype, device=q.device)
     if ws is None:
-        wb = lib().fb_attn_tree_workspace_bytes(Hq, kv, max_draft, width)
+        wb = _tree_workspace(dev, Hq, kv, max_draft, width)
         wp = None
         if wb:
             ws = torch.empty(wb, dtype=torch.uint8, device=q.device)

@@ -283,6 +283,21 @@ def test_binding_refuses_pitches_past_32_bits(sketched, far):
     assert sketched.calls[-1][0] == "fb_attn_tree" and sketched.calls[-1][2][1] == 2 ** 31 - 8
 
 
+@pytest.mark.parametrize("current", [0, 1])
+def test_workspace_is_that_of_the_tensors_device(sketched, current):
+    # its size goes by the SMs of the device that runs the call
+    bf = torch.bfloat16
+    sketched.current[0] = current
+    sketched._sizes["fb_attn_tree_workspace_bytes"] = 64
+    cache = tuple(Sketch((4, 2, 16, 64), bf, device=1) for _ in range(2))
+    q, out, lens = Sketch((2, 8, 64), bf, device=1), Sketch((2, 8, 64), bf, device=1), Sketch((2,), torch.int32, device=1)
+    assert fb.fb_attn_tree_workspace_bytes(8, cache, 1, 4) == 64
+    fb.fb_attn_tree(q, cache, Sketch((2, 4), torch.int32, device=1), lens, out=out)
+    assert [(name, device) for name, device, _ in sketched.calls] == [
+        ("fb_attn_tree_workspace_bytes", 1), ("fb_attn_tree_workspace_bytes", 1), ("fb_attn_tree", 1)]
+    assert sketched.calls[-1][2][-3] == 64 and sketched.current[0] == current
+
+
 def test_rope_frequencies():
     f = fb.rope_frequencies(8, 10000.0, device="cpu")
     assert f.dtype == torch.float64 and torch.allclose(f, torch.tensor([1.0, 0.1, 0.01, 0.001], dtype=torch.float64),

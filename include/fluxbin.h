@@ -367,7 +367,10 @@ FB_API fb_status fb_qk_norm_rope(const fb_heads *in, const fb_heads *out, const 
  * by at most 2^-8 (bf16) or 2^-11 (fp16) of their size, and as fp16 has few
  * exponents, there also by 2^-32 of the row's largest (weights below 2^-21 of
  * it lose bits, those below 2^-32 may be dropped).
- * An infinite or NaN score among those a row sees makes the row NaN. */
+ * A score that is NaN or plus infinity among those a row sees makes the row
+ * NaN; one of minus infinity has no weight, and a row of nothing else gives
+ * zeros and lse = -infinity.  An infinite value of a key that a row sees gives
+ * infinity or NaN (where the weight is rounded to zero). */
 FB_API fb_status fb_attn_prompt(const fb_heads *in, const int32_t *cu_seqlens, int n, float scale, void *out, int ldo,
                                 float *lse, unsigned flags, void *stream);
 
@@ -393,8 +396,8 @@ FB_API fb_status fb_attn_prompt(const fb_heads *in, const int32_t *cu_seqlens, i
  * of no sequence keep their contents.  Where a key head has at most 16 rows
  * (max_draft * Hq / Hkv) the weights are off by at most 2^-16 of their size
  * (fp16: and 2^-32 of the row's largest), with more rows they are rounded as in
- * fb_attn_prompt.  An infinite value among the committed keys gives infinity or
- * NaN.
+ * fb_attn_prompt.  Infinite and NaN scores and values among those a row sees
+ * are taken as there.
  * ws: fb_attn_tree_workspace_bytes bytes, 16-byte aligned, for the partial
  * results of sequences split over several CTAs; its contents need not be
  * set up and mean nothing afterwards, but calls that may run at the same

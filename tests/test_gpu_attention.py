@@ -325,6 +325,29 @@ def test_prompt_special_values_reach_only_rows_that_see_them(value, Hkv):
     assert torch.equal(got[:561][~hit[:561]], ref[:561][~hit[:561]]) and bool(torch.isnan(got[hit]).all())
 
 
+LOW = -30000.0   # a key of it against 1 scores below -3700: no weight, as one of minus infinity
+
+
+@pytest.mark.parametrize("H", [1, 200])
+@pytest.mark.parametrize("key", [0, 130])
+@pytest.mark.parametrize("D,dtype", [(64, torch.float16), (128, torch.bfloat16)])
+def test_prompt_infinite_scores(D, dtype, key, H):
+    n = 300
+    q, k, v, cu, cud = prompt_inputs([n], H, 1, D, dtype, seed=18)
+    q[..., 0] = torch.tensor([1.0, -1.0, 0.0], device=DEV)[torch.arange(n, device=DEV) % 3, None]
+    k[key, 0, 0] = LOW
+    low, k[key, 0, 0] = k.clone(), float("-inf")
+    lses = [torch.empty(n, H, device=DEV) for _ in range(2)]
+    want, got = (fb.fb_attn_prompt(q, x, v, cud, lse=y) for x, y in zip((low, k), lses))
+    i = torch.arange(n, device=DEV)
+    nan = (i >= key) & (i % 3 > 0)                       # plus infinity, and zero times infinity
+    same = ~nan & (i > 0) if key == 0 else ~nan
+    assert torch.equal(got[same], want[same]) and torch.equal(lses[1][same], lses[0][same])
+    assert bool(torch.isnan(got[nan]).all()) and bool(torch.isnan(lses[1][nan]).all())
+    if key == 0:                                         # nothing but minus infinity
+        assert not got[0].any() and bool((lses[1][0] == -float("inf")).all())
+
+
 def test_prompt_clamps_offsets_outside_the_tokens():
     q, k, v, cu, cud = prompt_inputs([40, 60], 2, 1, 64, torch.float16, seed=4)
     ref = fb.fb_attn_prompt(q, k, v, cud)
@@ -572,6 +595,29 @@ def test_tree_values_behind_the_keys_reach_no_row(Hq, D, page_size, dtype, garba
     for _ in range(20):
         again, _ = tree_call(c, None)
         assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("key", [100, 1999, 2002])
+@pytest.mark.parametrize("Hq,drafts,page_size", [(1, 8, 16), (1, 8, 4), (4, 8, 16), (4, 8, 4), (8, 8, 16), (8, 8, 4)])
+def test_tree_infinite_scores(Hq, drafts, page_size, key):
+    # committed or drafted; the second sequence's only key scores minus infinity, or plus, in every head
+    c = tree_inputs([2000, 0, 0], [drafts, 1, 1], Hq, 1, 64, page_size, torch.bfloat16, seed=19)
+    c["q"][:drafts:2, :, 0], c["q"][1:drafts:2, :, 0], c["q"][drafts:, :, 0] = 1, -1, 1
+    places = [(0, key, -1), (1, 0, -1), (2, 0, 1)]
+    k = [(int(c["table"][s, p // page_size]), 0, p % page_size, 0) for s, p, _ in places]
+    for at in k:
+        c["k"][at] = LOW
+    want, want_lse = tree_call(c)
+    for at, (_, _, sign) in zip(k, places):
+        c["k"][at] = sign * float("inf")
+    got, lse = tree_call(c)
+    for i in range(drafts):
+        if i % 2 == 0 or (key >= 2000 and not c["masks"][i] >> (key - 2000) & 1):
+            assert torch.equal(got[i], want[i]) and torch.equal(lse[i], want_lse[i])
+        else:
+            assert bool(torch.isnan(got[i]).all()) and bool(torch.isnan(lse[i]).all())
+    assert not got[drafts].any() and bool((lse[drafts] == -float("inf")).all())
+    assert bool(torch.isnan(got[drafts + 1]).all()) and bool(torch.isnan(lse[drafts + 1]).all())
 
 
 # up to 16 rows a key head, up to 32, more by each path

@@ -417,7 +417,8 @@ SINKS = [3.0, 18.3, 20.6, 22.4, 24.6, 25.5]
 def check_sinks(out, refs, octaves, most, D, dtype, w, what):
     for rows, head, (ro, rl, wabs, sabs), n in refs:
         e_p = 2 * sabs * (D + 2) * U + 2.0 ** -18
-        floor = 2.0 ** -32 * n * most * np.exp(octaves * np.log(2) - rl) if dtype == torch.float16 else 0 * rl
+        largest = 1.0 if octaves is None else np.exp(octaves * np.log(2) - rl)       # of the row's weights, at most
+        floor = 2.0 ** -32 * n * most * largest * (dtype == torch.float16)
         bound = HALF[dtype] * np.abs(ro) + (w + 2 * e_p + (n + 64) * U)[:, None] * wabs + floor[:, None] + TINY[dtype]
         assert_within(f64(out)[rows, head], ro, bound, f"{what}: head {head}")
 
@@ -566,6 +567,16 @@ def test_tree_small_weights_beside_sinks(Hq, drafts, page_size, dtype, octaves):
                 2.0 ** -16 if Hq * drafts <= 16 else HALF[dtype], "tree")
 
 
+@pytest.mark.parametrize("case", [t for t in TREES if t[2] // t[3] * max(t[1]) <= 16] +
+                         [([5000, 64, 1], [8, 1, 3], 4, 2, 128, 32, torch.bfloat16)],
+                         ids=lambda c: f"{len(c[0])}x{max(c[0])}+{max(c[1])}-{c[2]}/{c[3]}-{c[4]}-p{c[5]}-{str(c[6])[6:]}")
+def test_tree_weights_of_up_to_16_rows_lose_no_more_than_they_may(case):
+    c = tree_inputs(*case, seed=45)
+    out, _ = tree_call(c)
+    refs = tree_refs(c, c["masks"], c["D"] ** -0.5)
+    check_sinks(out, refs, None, 8.0, c["D"], c["dtype"], 2.0 ** -16, "few rows")    # no normal value reaches 8
+
+
 def test_tree_single_tokens_without_offsets():
     c = tree_inputs([70, 5], [1, 1], 4, 2, 64, 16, torch.float16, seed=1)
     a, _ = tree_call(c, None)
@@ -637,6 +648,45 @@ def test_tree_special_values_reach_only_rows_that_see_them(value, Hq, page_size)
             hit[i, Hq // 2:, 5] = True
     assert torch.equal(got[~hit], ref[~hit])
     assert bool((torch.isnan(got[hit]) if value != value else got[hit] == value).all())
+
+
+# one item of several pieces, the drafts on both sides of a tile's end; up to 16 rows a key head, up to 32, more
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("j", [3, 8])
+@pytest.mark.parametrize("Hq,page_size", [(1, 16), (1, 4), (2, 64), (2, 4), (8, 16), (8, 4)])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_tree_special_values_in_cut_items(dtype, Hq, page_size, j, value):
+    c = tree_inputs([4090, 70], [12, 1], Hq, 1, 64, page_size, dtype, seed=43)
+    ref, ref_lse = tree_call(c)
+    check_attention(ref, ref_lse, tree_refs(c, c["masks"], 64 ** -0.5, heads=[Hq - 1]), 64, dtype, "cut")
+    p = 4090 + j
+    c["v"][int(c["table"][0, p // page_size]), 0, p % page_size, 5] = value
+    got, lse = tree_call(c)
+    hit = torch.zeros(13, Hq, 64, dtype=torch.bool, device=DEV)
+    for i in range(12):
+        hit[i, :, 5] = bool(c["masks"][i] >> j & 1)
+    assert torch.equal(got[~hit], ref[~hit]) and torch.equal(lse, ref_lse)
+    assert bool((torch.isnan(got[hit]) if value != value else got[hit] == value).all())
+
+
+# heads that no tensor-core tile holds: the two-by-two warps, over pages of both forms
+@pytest.mark.parametrize("Hq,Hkv,D,page_size,dtype", [
+    (256, 1, 64, 16, torch.float16), (256, 1, 128, 64, torch.bfloat16), (160, 1, 128, 8, torch.bfloat16),
+    (1024, 4, 64, 32, torch.float16)])
+def test_tree_groups_of_more_than_128_heads(Hq, Hkv, D, page_size, dtype):
+    c = tree_inputs([70, 0, 900, 33], [2, 1, 3, 0], Hq, Hkv, D, page_size, dtype, seed=44)
+    out, lse = tree_call(c)
+    heads = [0, 63, 64, 129, Hq - 1]
+    check_attention(out, lse, tree_refs(c, c["masks"], D ** -0.5, heads=heads), D, dtype, "wide groups")
+    again, _ = tree_call(c, flags=fb.FB_GEMV_PDL)
+    assert torch.equal(again, out) and fb.fb_attn_errors() == 0
+    p = 900                                                               # the third sequence's first drafted token
+    c["v"][int(c["table"][2, p // page_size]), 0, p % page_size, 5] = float("nan")
+    got, _ = tree_call(c)
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    for i in range(3):
+        hit[3 + i, :Hq // Hkv, 5] = bool(c["masks"][3 + i] & 1)
+    assert torch.equal(got[~hit], out[~hit]) and bool(torch.isnan(got[hit]).all())
 
 
 @pytest.mark.parametrize("where", ["page", "negative", "width"])

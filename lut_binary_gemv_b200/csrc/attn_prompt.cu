@@ -14,7 +14,8 @@ namespace {
 
 // Up to this many full items for ten SMs, items are split.  Measured, split and not: 150 items, the longest of
 // 12,066 keys, 95 and 148 us; 75 items of up to 3,431 keys 30 and 47; 128 even items of 1,000 25 and 23; 256 even
-// items of 4,096 92 and 71 (each key tile then serves half as many queries).
+// items of 4,096 92 and 71 (each key tile then serves half as many queries).  The host knows the total of tokens and
+// not the lengths, so few even items are split too.
 constexpr int kSplitItems = 11;
 
 

@@ -29,8 +29,8 @@
 // soon as the product that reads the old weights has been issued.  The weights
 // come in two halves, so that the product starts before the second is there.
 //
-// Measured (16,384 tokens, 32 heads over 8 of 128, bf16): 1.69 ms, 1.30 PFLOP/s,
-// tensor cores 66% busy; a step of 128 keys and 256 queries takes 3,250 cycles:
+// Measured (16,384 tokens, 32 heads over 8 of 128, bf16): 1.69 ms, 1.30 PFLOP/s (once after a rest; back to back the
+// power cap makes it 1.93), tensor cores 66% busy; a step of 128 keys and 256 queries takes 3,250 cycles:
 // the chain of one tile (scores, 1,950 cycles of softmax, product, scores) is
 // what two tiles in turn do not quite hide.  K and V come from L2 (5.5 GB a
 // launch), not from HBM.

@@ -59,7 +59,7 @@ constexpr int kTileKeys = 64;      // keys of a tile, 16 loaded by each warp
 constexpr int kCtasPerSm = 2;
 __device__ unsigned int g_attn_errors;
 
-constexpr int kWholeKeys = 512;    // tables of no more keys: items are not cut
+constexpr int kWholeKeys = 512;    // tables of no more keys: items are not cut (the host does not know the lengths)
 
 // What starting and ending a piece costs, in key tiles.
 template <int MT>
